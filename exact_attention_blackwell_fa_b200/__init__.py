@@ -13,6 +13,13 @@ library's CUDA kernels.  The functions carry the C names:
                   max_seqlen_k, seqused_k=None, causal=False, scale=None) -> (dq, dk, dv)
     fa_bwd_workspace_size(B, Sq, Hq, d) -> int
     fa_bwd_noalloc(q, k, v, o, lse, dout, causal=False, scale=None) -> (dq, dk, dv)
+    fa_kv_cache_size(num_pages, page_size, Hkv, d, fmt=FA_KV_16) -> int
+    fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, inv_freq=None,
+                 interleaved=False) -> q_out        # rotates q and k, fills the paged caches
+    fa_kv_gather(k_cache, v_cache, cu_seqlens_k, block_table, total_k, dtype=None) -> (k, v)
+    fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q,
+                 causal=False, scale=None) -> (o, lse)
+    fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d) -> int
     fa_status_string(code) -> str
     fa_last_device_status() -> (code, detail)
     fa_clear_device_status()
@@ -36,11 +43,13 @@ from . import _lib
 
 __all__ = [
     "FAError", "fa_fwd", "fa_fwd_splitkv", "fa_fwd_varlen", "fa_bwd", "fa_bwd_varlen", "fa_bwd_noalloc", "fa_bwd_workspace_size", "fa_status_string",
+    "fa_kv_cache_size", "fa_kv_append", "fa_kv_gather", "fa_fwd_paged", "fa_fwd_paged_workspace_size", "FA_KV_16", "FA_KV_INT4",
     "fa_last_device_status", "fa_clear_device_status", "fa_set_unit_schedule", "fa_set_exp2_emulation", "fa_set_wait_timeout_ms", "fa_debug_inject", "fa_debug_exp2",
     "FA_SCHED_STATIC", "FA_SCHED_CLC", "FA_SCHED_AUTO",
 ]
 
 FA_SCHED_STATIC, FA_SCHED_CLC, FA_SCHED_AUTO = 0, 1, 2
+FA_KV_16, FA_KV_INT4 = _lib.FA_KV_16, _lib.FA_KV_INT4
 
 
 class FAError(RuntimeError):
@@ -315,6 +324,171 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool = False, scale: float | N
                                           _stream_ptr(stream))
     _raise(code, "fa_bwd_noalloc")
     return dq, dk, dv
+
+
+def fa_kv_cache_size(num_pages: int, page_size: int, Hkv: int, d: int, fmt: int = FA_KV_16) -> int:
+    """Bytes of one pool of the paged cache (keys or values); 0 for unsupported sizes."""
+    return int(_lib.load().fa_kv_cache_size(num_pages, page_size, Hkv, d, fmt))
+
+
+def _check_cache(k_cache, v_cache, dtype, block_table, ref, **index):
+    """Validates a pair of pools and the int32 index arrays of a paged-cache call; returns
+    (num_pages, Hkv, page_size, d, fmt, B, max_pages).  Pools are [num_pages, Hkv,
+    page_size, d] in the call's dtype, or uint8 [num_pages, Hkv, page_size, 5 d / 8]."""
+    _check(k_cache, "k_cache")
+    _check(v_cache, "v_cache", k_cache.dtype)
+    int4 = k_cache.dtype == torch.uint8
+    if not int4 and k_cache.dtype != dtype:
+        raise ValueError(f"fa: k_cache has dtype {k_cache.dtype}, expected {dtype} or uint8")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("fa: k_cache and v_cache must be [num_pages, Hkv, page_size, d] (4-bit: 5 d / 8 bytes)")
+    num_pages, Hkv, page_size, width = k_cache.shape
+    if int4 and width % 5:
+        raise ValueError(f"fa: a 4-bit pool has 5 d / 8 bytes per token, got {width}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("fa: block_table must be a [B, max_pages] tensor")
+    B, max_pages = block_table.shape
+    for name, t, n in (("block_table", block_table, None), ("seqlens_k", index.get("seqlens_k"), B),
+                       (index["cu_name"], index["cu"], B + 1)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.device != ref.device or t.dtype != torch.int32 or \
+                not t.is_contiguous():
+            raise ValueError(f"fa: {name} must be a contiguous int32 tensor on {ref.device}")
+        if n is not None and t.shape != (n,):
+            raise ValueError(f"fa: {name} has shape {tuple(t.shape)}, expected ({n},)")
+    _same_device(ref, k_cache=k_cache, v_cache=v_cache)
+    return (num_pages, Hkv, page_size, width * 8 // 5 if int4 else width, FA_KV_INT4 if int4 else FA_KV_16, B,
+            max_pages)
+
+
+def _token_rows(t, name, H, d):
+    """A packed [total, H, d] tensor whose rows may lie apart (a slice of a fused
+    projection); returns the distance between rows in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"fa: {name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1:] != (H, d):
+        raise ValueError(f"fa: {name} has shape {tuple(t.shape)}, expected (total, {H}, {d})")
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"fa: the heads of a row of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else H * d
+
+
+def fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, inv_freq=None,
+                 interleaved: bool = False, q_out=None, stream=None):
+    """Appends a step's packed tokens to a paged cache: rotates q [total,Hq,d] and k
+    [total,Hkv,d] by their positions (pairs of the first 2 * len(inv_freq) head dims;
+    inv_freq float32 CUDA or None) and writes k and v to their pages.  cu_seqlens [B+1]:
+    the new tokens per sequence; seqlens_k [B]: its cached tokens, the new ones included;
+    block_table [B,max_pages].  q, k, v may be slices of a fused projection.  q may be
+    None.  Returns the rotated q [total,Hq,d]."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("fa: k must be [total, Hkv, d]")
+    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(
+        k_cache, v_cache, k.dtype, block_table, k, seqlens_k=seqlens_k, cu_name="cu_seqlens", cu=cu_seqlens)
+    dt = _dtype_code(k)
+    k_stride, v_stride = _token_rows(k, "k", Hkv, d), _token_rows(v, "v", Hkv, d)
+    total = k.shape[0]
+    Hq, q_stride = Hkv, Hkv * d
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("fa: q must be [total, Hq, d]")
+        Hq = q.shape[1]
+        q_stride = _token_rows(q, "q", Hq, d)
+        if q_out is None:
+            q_out = torch.empty(total, Hq, d, dtype=q.dtype, device=q.device)
+        _check(q_out, "q_out", k.dtype)
+        _shape(q_out, "q_out", (total, Hq, d))
+    elif q_out is not None:
+        raise ValueError("fa: q_out without q")
+    for name, t in (("q", q), ("v", v)):
+        if t is not None and (t.dtype != k.dtype or t.shape[0] != total):
+            raise ValueError(f"fa: {name} has {t.shape[0]} rows of {t.dtype}, expected {total} of {k.dtype}")
+    rot = 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32)
+        rot = 2 * inv_freq.numel()
+    _same_device(k, q=q, v=v, q_out=q_out, inv_freq=inv_freq)
+    with torch.cuda.device(k.device):
+        code = _lib.load().fa_kv_append(
+            q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
+            q_out.data_ptr() if q is not None else None, k_cache.data_ptr(), v_cache.data_ptr(),
+            cu_seqlens.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(),
+            inv_freq.data_ptr() if rot else None, rot, int(bool(interleaved)), B, total, Hq, Hkv, d, page_size,
+            num_pages, max_pages, fmt, dt, _stream_ptr(stream))
+    _raise(code, "fa_kv_append")
+    return q_out
+
+
+def fa_kv_gather(k_cache, v_cache, cu_seqlens_k, block_table, total_k: int, dtype=None, k=None, v=None,
+                 stream=None):
+    """Reads the first cu_seqlens_k[b+1] - cu_seqlens_k[b] cached tokens of every sequence
+    back as packed rows -> (k, v) [total_k,Hkv,d].  dtype: the type of a 4-bit pool's
+    scales and of its rows (a 16-bit pool has its own)."""
+    _check(k_cache, "k_cache")
+    if k_cache.dtype != torch.uint8:
+        dtype = k_cache.dtype if dtype is None else dtype
+    elif dtype is None:
+        raise ValueError("fa: a 4-bit pool needs the dtype of its scales")
+    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(
+        k_cache, v_cache, dtype, block_table, k_cache, cu_name="cu_seqlens_k", cu=cu_seqlens_k)
+    total_k = int(total_k)
+    shape = (total_k, Hkv, d)
+    k = torch.empty(shape, dtype=dtype, device=k_cache.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=k_cache.device) if v is None else v
+    dt = _dtype_code(k)
+    for name, t in (("k", k), ("v", v)):
+        _check(t, name, dtype)
+        _shape(t, name, shape)
+    _same_device(k_cache, k=k, v=v)
+    with torch.cuda.device(k_cache.device):
+        code = _lib.load().fa_kv_gather(k_cache.data_ptr(), v_cache.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                        cu_seqlens_k.data_ptr(), block_table.data_ptr(), B, total_k, Hkv, d,
+                                        page_size, num_pages, max_pages, fmt, dt, _stream_ptr(stream))
+    _raise(code, "fa_kv_gather")
+    return k, v
+
+
+def fa_fwd_paged_workspace_size(B: int, max_seqlen_q: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(_lib.load().fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d))
+
+
+def fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q: int,
+                 causal: bool = False, scale: float | None = None, out=None, lse=None, workspace=None,
+                 stream=None):
+    """Forward over a paged cache (decoding and short chunks).  q [total_q,Hq,d], pools
+    as fa_kv_append fills them, seqlens_k [B] cached tokens per sequence
+    -> (o [total_q,Hq,d], lse [Hq,total_q] fp32)."""
+    _check(q, "q")
+    if q.dim() != 3:
+        raise ValueError("fa: q must be [total_q, Hq, d]")
+    total_q, Hq, d = q.shape
+    num_pages, Hkv, page_size, dk, fmt, B, max_pages = _check_cache(
+        k_cache, v_cache, q.dtype, block_table, q, seqlens_k=seqlens_k, cu_name="cu_seqlens_q", cu=cu_seqlens_q)
+    if dk != d:
+        raise ValueError(f"fa: the pools hold head_dim {dk}, q has {d}")
+    dt = _dtype_code(q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = torch.empty_like(q) if out is None else out
+    if lse is None:
+        lse = torch.empty(Hq, total_q, dtype=torch.float32, device=q.device)
+    _check(out, "out", q.dtype)
+    _check(lse, "lse", torch.float32)
+    _shape(out, "out", q.shape)
+    _shape(lse, "lse", (Hq, total_q))
+    _same_device(q, out=out, lse=lse)
+    lib = _lib.load()
+    with torch.cuda.device(q.device):
+        workspace = _workspace(workspace, q, int(lib.fa_fwd_paged_workspace_size(B, int(max_seqlen_q), Hq, Hkv, d)))
+        code = lib.fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+                                lse.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
+                                block_table.data_ptr(), B, int(max_seqlen_q), total_q, Hq, Hkv, d, page_size,
+                                num_pages, max_pages, fmt, int(bool(causal)), float(scale), dt,
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                _stream_ptr(stream))
+    _raise(code, "fa_fwd_paged")
+    return out, lse
 
 
 def fa_last_device_status(stream=None):

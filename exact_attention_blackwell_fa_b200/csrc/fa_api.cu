@@ -14,6 +14,7 @@
 #include "fa_bwd.cuh"
 #include "fa_bwd_wide.cuh"
 #include "fa_fwd.cuh"
+#include "fa_host.h"
 
 namespace {
 
@@ -55,34 +56,10 @@ bool make_tmap(CUtensorMap* m, const void* ptr, int B, int S, int H, int d, bool
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct DeviceInfo {
-    int sm_count = 0;
-    bool ok = false;  // compute capability 10.0 (B200 class, sm_100a code runs)
-};
-
-constexpr int kMaxDevices = 64;
-
-fa_status device_info(DeviceInfo* out)
-{
-    static DeviceInfo cache[kMaxDevices];
-    static std::mutex mu;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(mu);
-    if (cache[dev].sm_count == 0) {
-        int major = 0, minor = 0, sms = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return FA_ERR_CUDA;
-        cache[dev].sm_count = sms;
-        cache[dev].ok = (major == 10 && minor == 0);
-    }
-    *out = cache[dev];
-    return out->ok ? FA_OK : FA_ERR_UNSUPPORTED;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using fa::aligned16;
+using fa::device_info;
+using fa::DeviceInfo;
+using fa::kMaxDevices;
 
 fa_status check_common(int B, int Sq, int Sk, int Hq, int Hkv, int d, float scale, fa_dtype dt)
 {
@@ -589,27 +566,31 @@ const char* fa_status_string(fa_status s)
     case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT: a kernel gave up on a bounded wait";
     case FA_ERR_SCRATCH_LIMIT:
         return "FA_ERR_SCRATCH_LIMIT: problem needs more scratch than fa_bwd_noalloc's built-in array";
+    case FA_ERR_BAD_PAGE:
+        return "FA_ERR_BAD_PAGE: a block table entry or cached length points outside the page pool";
     }
     return "unknown fa_status";
 }
 
 fa_status fa_last_device_status(fa_stream stream, uint32_t* detail)
 {
-    uint32_t h[4] = {0, 0, 0, 0};
+    uint32_t h[4] = {0, 0, 0, 0}, paged[4] = {0, 0, 0, 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaMemcpyFromSymbolAsync(h, fa::g_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s) !=
             cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
+        fa::paged_status_read(paged, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return FA_ERR_CUDA;
-    if (detail) *detail = h[1];
-    return static_cast<fa_status>(h[0]);
+    const uint32_t* first = h[0] ? h : paged;
+    if (detail) *detail = first[1];
+    return static_cast<fa_status>(first[0]);
 }
 
 fa_status fa_clear_device_status(fa_stream stream)
 {
     static const uint32_t zero[4] = {0, 0, 0, 0};
     return cudaMemcpyToSymbolAsync(fa::g_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess &&
+                   fa::paged_status_clear(reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }

@@ -50,7 +50,9 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,    /* head_dim, dtype or GPU architecture not supported       */
     FA_ERR_CUDA = 3,           /* a CUDA runtime/driver call failed                       */
     FA_ERR_DEVICE_TIMEOUT = 4, /* a kernel gave up on a bounded wait (see status query)   */
-    FA_ERR_SCRATCH_LIMIT = 5   /* problem needs more than the built-in scratch array      */
+    FA_ERR_SCRATCH_LIMIT = 5,  /* problem needs more than the built-in scratch array      */
+    FA_ERR_BAD_PAGE = 6        /* device status: a block table entry or a cached length
+                                  points outside the page pool                            */
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
@@ -172,6 +174,92 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                          fa_dtype dt, fa_stream stream);
 
 /*
+ * Paged KV cache, for serving.  The keys of all sequences live in one pool of pages and
+ * the values in another; page_size (16, 32, 64, 128 or 256) tokens share a page, and
+ * row b of block_table [B, max_pages] lists the pages of sequence b in order, so its
+ * token j is in page block_table[b * max_pages + j / page_size], slot j % page_size.
+ * Two pool formats, the same for keys and values:
+ *   FA_KV_16:   [num_pages, Hkv, page_size, d] in the call's dtype;
+ *   FA_KV_INT4: per (page, head) page_size * 5 d / 8 bytes: first the codes, page_size
+ *     rows of d / 2 bytes (dim 2 i in the low four bits of byte i, dim 2 i + 1 in the
+ *     high four), then page_size rows of d / 32 (scale, zero) pairs in the call's dtype.
+ *     A group of 32 head dims shares a pair; its code c stands for scale * c + zero.
+ *     On writing, zero is the group's least value and scale a fifteenth of what the
+ *     greatest lies above that zero, each rounded to the dtype, and c the nearest whole
+ *     number (ties to even, 0 to 15) of scales above the zero.  A group that holds an
+ *     infinity or a NaN, or whose scale or zero rounds to one, reads back as NaN.
+ * Pools are addressed with 64-bit offsets.  block_table, seqlens_k and the cu_seqlens
+ * arrays are device int32 arrays that the host does not read, so a captured graph can
+ * be replayed with new lengths and pages (max_seqlen_q and the row totals of a call
+ * stay as captured).  seqlens_k[b] counts the cached tokens of sequence b, those of this
+ * step included: of its n_b = cu_seqlens[b+1] - cu_seqlens[b] new tokens, the i-th is
+ * token seqlens_k[b] - n_b + i of the sequence.  Rows of the packed tensors that belong
+ * to no sequence (past cu_seqlens[B]) are neither read nor written.  A call with no
+ * packed rows at all is valid and does nothing.
+ *
+ * A token whose block table entry is not a page of the pool, or whose position is not
+ * in the table (negative, or max_pages * page_size and up), is not written by
+ * fa_kv_append, reads as zeros in fa_kv_gather and is left out of fa_fwd_paged; nothing
+ * outside the pool is touched, and the device status becomes FA_ERR_BAD_PAGE.
+ */
+typedef enum { FA_KV_16 = 0, FA_KV_INT4 = 1 } fa_kv_format;
+
+/* Bytes of one pool (keys or values); 0 for sizes that no call takes. */
+size_t fa_kv_cache_size(int num_pages, int page_size, int Hkv, int d, fa_kv_format fmt);
+
+/*
+ * Appends a step's new tokens: rotates their queries and keys by their positions, writes
+ * the queries to q_out [total, Hq, d] and the keys and values to their places in the
+ * pools.  q [total, Hq, d] and k, v [total, Hkv, d] hold the packed tokens (cu_seqlens:
+ * B + 1 nondecreasing offsets from 0); row t of each starts q_stride, k_stride, v_stride
+ * elements after row t - 1 (multiples of 8, at least the row's size), so that they can
+ * be slices of a fused projection.  q and q_out may both be NULL: keys and values only.
+ * q_out may be q itself (with q_stride = Hq * d); otherwise the outputs overlap no input.
+ * Rotation: with position p, pair r < rot_dim / 2 of the first rot_dim head dims turns
+ * by the angle p * inv_freq[r] (radians; inv_freq a device float32 array):
+ *     (x, y) -> (x cos - y sin, y cos + x sin),
+ * the pair being dims (r, r + rot_dim / 2), or (2 r, 2 r + 1) with interleaved != 0.
+ * rot_dim: a multiple of 16 from 0 (no rotation; inv_freq may be NULL) to d.  The angle
+ * is reduced exactly, at any position.  Values are rounded once, after the rotation
+ * (a 4-bit pool takes the unrounded rotated key).  Tokens of one call must not share a
+ * place in the pools.
+ */
+fa_status fa_kv_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                       long long v_stride, void* q_out, void* k_cache, void* v_cache, const int* cu_seqlens,
+                       const int* seqlens_k, const int* block_table, const float* inv_freq, int rot_dim,
+                       int interleaved, int B, int total, int Hq, int Hkv, int d, int page_size, int num_pages,
+                       int max_pages, fa_kv_format fmt, fa_dtype dt, fa_stream stream);
+
+/*
+ * Reads cached tokens back as packed rows: rows cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1
+ * of k, v [total_k, Hkv, d] become tokens 0, 1, ... of sequence b (4-bit values rounded
+ * once to the dtype).  With fa_kv_append before it, this gives fa_fwd_varlen the keys
+ * and values for a prompt's next chunk over its cached prefix.
+ */
+fa_status fa_kv_gather(const void* k_cache, const void* v_cache, void* k, void* v, const int* cu_seqlens_k,
+                       const int* block_table, int B, int total_k, int Hkv, int d, int page_size, int num_pages,
+                       int max_pages, fa_kv_format fmt, fa_dtype dt, fa_stream stream);
+
+/*
+ * Forward over a paged cache, for decoding and short chunks: the queries of sequence b
+ * (rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of q, o [total_q, Hq, d]; lse float32
+ * [Hq, total_q]) attend over its seqlens_k[b] cached tokens, the causal mask aligned to
+ * the bottom right as everywhere.  A negative seqlens_k[b] counts as 0, one beyond the
+ * table as max_pages * page_size (with the device status set).  max_seqlen_q bounds the
+ * queries per sequence (longer ones are cut to it).  A row that sees no key gets O = 0
+ * and LSE = -inf.  What the pools hold past a sequence's end is not used.  `workspace` is caller-owned device memory
+ * of at least fa_fwd_paged_workspace_size(...) bytes, 256-byte aligned (NULL when that
+ * is 0); its contents on entry do not matter, and calls that overlap on the GPU need
+ * one each.  Repeated calls give the same bits.
+ */
+size_t fa_fwd_paged_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int d);
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                       const int* cu_seqlens_q, const int* seqlens_k, const int* block_table, int B,
+                       int max_seqlen_q, int total_q, int Hq, int Hkv, int d, int page_size, int num_pages,
+                       int max_pages, fa_kv_format fmt, int causal, float scale, fa_dtype dt, void* workspace,
+                       size_t workspace_bytes, fa_stream stream);
+
+/*
  * exp2 split of the forward's softmax ("FlashAttention 4: Snellere,
  * Geheugenefficiente Aandacht voor LLM's", section "Software-exponentials via
  * CUDA-kernen": part of the exponentials go to a cubic polynomial on the FMA pipe
@@ -191,11 +279,11 @@ fa_status fa_set_exp2_emulation(int pairs_of_4);
 const char* fa_status_string(fa_status s);
 
 /*
- * Device-side status of the kernels run so far on this device: FA_OK, or
+ * Device-side status of the kernels run so far on this device: FA_OK,
  * FA_ERR_DEVICE_TIMEOUT if some kernel gave up on a bounded wait (each wait in
  * the kernels gives up after the limit of fa_set_wait_timeout_ms, one second by
- * default).  Synchronises `stream` to read it.  `detail` (may be NULL) receives a
- * code naming the wait that gave up.  After a timeout the outputs of the calls
+ * default), or FA_ERR_BAD_PAGE if a paged-cache call met a token outside the pool.  Synchronises `stream` to read it.  `detail` (may be NULL) receives a
+ * code naming the wait that gave up (or the paged-cache call).  After a timeout the outputs of the calls
  * since the last clear are invalid; the context stays usable.
  */
 fa_status fa_last_device_status(fa_stream stream, uint32_t* detail);
