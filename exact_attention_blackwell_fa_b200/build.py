@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = {
     "fa_api.cu": ["fa_host.h", "fa_fwd.cuh", "fa_bwd.cuh", "fa_bwd_wide.cuh", "fa_common.cuh", "sm100.cuh",
                   "exp2_poly.h"],
-    "fa_paged.cu": ["fa_host.h", "fa_paged.cuh", "sm100.cuh"],
+    "fa_paged.cu": ["fa_host.h", "fa_paged.cuh", "fa_paged_fwd.cuh", "sm100.cuh"],
 }
 OBJ = os.path.join(CSRC, "_build")
 

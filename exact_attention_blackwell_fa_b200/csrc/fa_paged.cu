@@ -5,6 +5,7 @@
 
 #include "fa_host.h"
 #include "fa_paged.cuh"
+#include "fa_paged_fwd.cuh"
 
 namespace fa {
 
@@ -77,18 +78,80 @@ fa_status launch_gather(const fa::GatherParams& p, unsigned blocks, bool bf16, b
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int D>
-fa_status launch_paged(const fa::PagedFwdParams& p, bool bf16, bool int4, cudaStream_t s)
+// Eight-row tiles of a unit: the fewest that hold the rows of a sequence at once, as far
+// as a warp's registers go (O^T takes NT * D / 4 of them).  A wider unit reads the pages
+// for more rows at a time.
+int paged_tiles(int max_q, int group, int d)
 {
-    const dim3 grid(p.total_q, p.Hq);
-    if (int4) {
-        if (bf16) fa::fa_fwd_paged_kernel<D, true, true><<<grid, 128, 0, s>>>(p);
-        else fa::fa_fwd_paged_kernel<D, false, true><<<grid, 128, 0, s>>>(p);
-    } else {
-        if (bf16) fa::fa_fwd_paged_kernel<D, true, false><<<grid, 128, 0, s>>>(p);
-        else fa::fa_fwd_paged_kernel<D, false, false><<<grid, 128, 0, s>>>(p);
+    const long long rows = static_cast<long long>(max_q) * group;
+    const int most = d == 128 ? 4 : d <= 256 ? 2 : 1;
+    int nt = 1;
+    while (nt < most && 8 * nt < rows) nt *= 2;
+    return nt;
+}
+
+// Resident CTAs of the forward's grid, at most: two per SM.
+int paged_grid_max(int sm_count) { return 2 * sm_count; }
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t paged_workspace(int sm_count, int rows, int d, fa::PagedFwdParams* p, void* ws)
+{
+    const size_t n = paged_grid_max(sm_count);
+    const size_t o = round256(2 * n * rows * d * 4), ml = round256(2 * n * rows * 8), rec = round256(n * sizeof(fa::PagedRecord));
+    if (p) {
+        uint8_t* w = static_cast<uint8_t*>(ws);
+        p->opart = reinterpret_cast<float*>(w);
+        p->mlpart = reinterpret_cast<float2*>(w + o);
+        p->rec = reinterpret_cast<fa::PagedRecord*>(w + o + ml);
     }
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return o + ml + rec;
+}
+
+template <int D, bool BF16, bool INT4, int NT>
+fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s)
+{
+    using C = fa::PagedCfg<D, INT4, NT>;
+    auto kernel = fa::fa_fwd_paged_kernel<D, BF16, INT4, NT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        return FA_ERR_CUDA;
+    // no more CTAs than there can be granules
+    const long long blocks = (static_cast<long long>(p.max_q) * p.group + C::ROWS - 1) / C::ROWS;
+    const long long keys = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
+    const double most = static_cast<double>(p.B) * blocks * p.pool.Hkv * ((keys + C::GR - 1) / C::GR);
+    int grid = C::CTAS * sm_count;
+    if (most < grid) grid = static_cast<int>(most);
+    kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // the join starts its blocks while the forward's last CTAs run, and waits for them
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, C::ROWS);
+    cfg.blockDim = dim3(fa::kJoinWarps * 32);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa::fa_fwd_paged_join_kernel<D, BF16, C::ROWS>, p, grid) == cudaSuccess ? FA_OK
+                                                                                                           : FA_ERR_CUDA;
+}
+
+template <int D, int NT>
+fa_status launch_paged_types(const fa::PagedFwdParams& p, bool bf16, bool int4, int sm_count, cudaStream_t s)
+{
+    if (int4) return bf16 ? launch_paged<D, true, true, NT>(p, sm_count, s) : launch_paged<D, false, true, NT>(p, sm_count, s);
+    return bf16 ? launch_paged<D, true, false, NT>(p, sm_count, s) : launch_paged<D, false, false, NT>(p, sm_count, s);
+}
+
+template <int D>
+fa_status launch_paged_rows(const fa::PagedFwdParams& p, int nt, bool bf16, bool int4, int sm_count, cudaStream_t s)
+{
+    if constexpr (D == 128)
+        if (nt == 4) return launch_paged_types<D, 4>(p, bf16, int4, sm_count, s);
+    if constexpr (D <= 256)
+        if (nt == 2) return launch_paged_types<D, 2>(p, bf16, int4, sm_count, s);
+    return launch_paged_types<D, 1>(p, bf16, int4, sm_count, s);
 }
 
 }  // namespace
@@ -196,12 +259,10 @@ fa_status fa_kv_gather(const void* k_cache, const void* v_cache, void* k, void* 
 
 size_t fa_fwd_paged_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int d)
 {
-    (void)B;
-    (void)max_seqlen_q;
-    (void)Hq;
-    (void)Hkv;
-    (void)d;
-    return 0;
+    if (B < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim_ok(d)) return 0;
+    DeviceInfo di;
+    if (device_info(&di) != FA_OK) return 0;
+    return paged_workspace(di.sm_count, 8 * paged_tiles(max_seqlen_q, Hq / Hkv, d), d, nullptr, nullptr);
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
@@ -217,14 +278,15 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     if (!cu_seqlens_q || !seqlens_k || !aligned4(cu_seqlens_q) || !aligned4(seqlens_k)) return FA_ERR_INVALID_ARG;
     if (max_seqlen_q < 1 || total_q < 0 || Hq < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
-    if (static_cast<long long>(total_q) * Hq >= (1LL << 31) || Hq > 65535) return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(total_q) * Hq >= (1LL << 31)) return FA_ERR_INVALID_ARG;
     if (total_q == 0) return FA_OK;
     if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_INVALID_ARG;
     DeviceInfo di;
     st = device_info(&di);
     if (st != FA_OK) return st;
+    const int nt = paged_tiles(max_seqlen_q, Hq / Hkv, d);
+    if (workspace_bytes < paged_workspace(di.sm_count, 8 * nt, d, &p, workspace)) return FA_ERR_INVALID_ARG;
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -242,11 +304,11 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     const bool bf16 = dt == FA_BF16, int4 = fmt == FA_KV_INT4;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (d) {
-    case 128: return launch_paged<128>(p, bf16, int4, s);
-    case 192: return launch_paged<192>(p, bf16, int4, s);
-    case 256: return launch_paged<256>(p, bf16, int4, s);
-    case 384: return launch_paged<384>(p, bf16, int4, s);
-    default: return launch_paged<512>(p, bf16, int4, s);
+    case 128: return launch_paged_rows<128>(p, nt, bf16, int4, di.sm_count, s);
+    case 192: return launch_paged_rows<192>(p, nt, bf16, int4, di.sm_count, s);
+    case 256: return launch_paged_rows<256>(p, nt, bf16, int4, di.sm_count, s);
+    case 384: return launch_paged_rows<384>(p, nt, bf16, int4, di.sm_count, s);
+    default: return launch_paged_rows<512>(p, nt, bf16, int4, di.sm_count, s);
     }
 }
 

@@ -1,5 +1,5 @@
 // fa_paged.cuh -- the paged KV cache's kernels: append (rotation by position, 16-bit or
-// 4-bit pages), read-back, and attention over the pages.
+// 4-bit pages) and read-back.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -400,13 +400,6 @@ __device__ __forceinline__ uint4 read_vector(const uint8_t* blk, const PoolView&
 }
 
 template <int D, bool BF16, bool INT4>
-__device__ __forceinline__ void read_values(const uint8_t* blk, const PoolView& v, int slot, int u, float (&x)[8])
-{
-    if constexpr (INT4) read_codes<D, BF16>(blk, v, slot, u, x);
-    else pg_unpack8<BF16>(read_vector<D, BF16, false>(blk, v, slot, u), x);
-}
-
-template <int D, bool BF16, bool INT4>
 __global__ void __launch_bounds__(256) fa_kv_gather_kernel(const GatherParams p)
 {
     constexpr int VPR = D / 8;
@@ -441,96 +434,6 @@ __global__ void __launch_bounds__(256) fa_kv_gather_kernel(const GatherParams p)
         reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? p.k : p.v) +
                                  (static_cast<size_t>(t0 + i) * p.pool.Hkv + h) * D)[u] = x;
     }
-}
-
-// ---------------------------------------------------------------------------------
-// Attention over the pages: one block per (packed query row, query head), 128 keys at a
-// time with an online softmax.
-// ---------------------------------------------------------------------------------
-struct PagedFwdParams {
-    const void* q;
-    const void *k_cache, *v_cache;
-    void* o;
-    float* lse;
-    const int *cu_q, *seqlens_k;
-    PoolView pool;
-    int B, max_q, total_q, Hq, group, causal;
-    float sl2;  // scale * log2(e)
-};
-
-template <int D, bool BF16, bool INT4>
-__global__ void __launch_bounds__(128) fa_fwd_paged_kernel(const PagedFwdParams p)
-{
-    constexpr int VPR = D / 8;
-    __shared__ int seq;
-    __shared__ float sq[D], sp[128], red[4];
-    __shared__ int spage[128];
-    const int t = blockIdx.x, h = blockIdx.y, hkv = h / p.group, tid = threadIdx.x;
-    if (tid == 0) seq = -1;
-    __syncthreads();
-    find_sequences(p.cu_q, p.B, t, 1, &seq);
-    __syncthreads();
-    if (seq < 0) return;
-    const int b = seq, i = t - p.cu_q[b];
-    const int Sq = min(p.cu_q[b + 1] - p.cu_q[b], p.max_q);
-    if (i >= Sq) return;
-    const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
-    const int Sk = max(0, static_cast<int>(min(static_cast<long long>(p.seqlens_k[b]), room)));
-    if (tid == 0 && p.seqlens_k[b] > room) record_bad_page(PAGED_FWD);
-    const int lim = p.causal ? min(Sk, i + Sk - Sq + 1) : Sk;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(t) * p.Hq + h) * D;
-    for (int c = tid; c < D; c += 128) sq[c] = pg_unpack2<BF16>(q[c]).x * p.sl2;
-    float m = -INFINITY, l = 0.0f, acc[D / 128 + 1] = {};
-    for (int j0 = 0; j0 < lim; j0 += 128) {
-        __syncthreads();
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        int page = -1;
-        if (j < lim) {
-            page = pool_page(p.pool, b, j);
-            if (page < 0) record_bad_page(PAGED_FWD);
-            else {
-                const uint8_t* blk = static_cast<const uint8_t*>(p.k_cache) + pool_block<D, INT4>(p.pool, page, hkv);
-                s = 0.0f;
-                for (int u = 0; u < VPR; ++u) {
-                    float x[8];
-                    read_values<D, BF16, INT4>(blk, p.pool, j & (p.pool.page_size - 1), u, x);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) s = fmaf(x[c], sq[8 * u + c], s);
-                }
-            }
-        }
-        spage[tid] = page;
-        float mx = s;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float alpha = exp2f(m - ref);
-        sp[tid] = exp2f(s - ref);
-        m = mn;
-        __syncthreads();
-        l *= alpha;
-        for (int c = 0; c < D / 128 + 1; ++c) acc[c] *= alpha;
-        for (int k = 0; k < min(128, lim - j0); ++k) {
-            const float w = sp[k];
-            l += w;
-            if (spage[k] < 0) continue;
-            const uint8_t* blk = static_cast<const uint8_t*>(p.v_cache) + pool_block<D, INT4>(p.pool, spage[k], hkv);
-            const int slot = (j0 + k) & (p.pool.page_size - 1);
-            for (int c = tid, n = 0; c < D; c += 128, ++n) {
-                float x[8];
-                read_values<D, BF16, INT4>(blk, p.pool, slot, c >> 3, x);
-                acc[n] = fmaf(w, x[c & 7], acc[n]);
-            }
-        }
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    uint16_t* o = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(t) * p.Hq + h) * D;
-    for (int c = tid, n = 0; c < D; c += 128, ++n) o[c] = static_cast<uint16_t>(pg_pack2<BF16>(acc[n] * inv, 0.0f));
-    if (tid == 0)
-        p.lse[static_cast<size_t>(h) * p.total_q + t] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace fa

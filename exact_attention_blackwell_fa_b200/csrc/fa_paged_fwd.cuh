@@ -1,0 +1,948 @@
+// fa_paged_fwd.cuh -- attention over the paged cache, for few query rows per sequence.
+//
+//   O = softmax(scale Q K^T [+ causal]) V, LSE, K and V read from the pools.
+//
+// Bound by memory: every cached token is read once for all the query heads that share
+// its KV head, and a decode step does only 2 * group products per cached value.  So:
+//
+//   * a work unit is (sequence, block of 8 NT query rows, KV head), its rows being
+//     (query, head of the group) pairs; a unit's keys are cut into granules of W * TS
+//     tokens, and the granules of all units, in order, into as many equal ranges as
+//     there are resident CTAs -- whatever the lengths, every CTA streams the same
+//     number of tokens.  Lengths are read on the device.  A unit that falls into one
+//     range is written directly; the pieces of one that was cut go to the workspace in
+//     fp32 and a second, small launch joins them in a fixed order;
+//   * each warp streams its own TS tokens of a granule through its own ring of
+//     shared-memory slots with cp.async (rows past the end or without a page are filled
+//     with zeros, so nothing a pool holds there can reach a sum) and keeps its own
+//     running maximum, sum and O; the warps of a CTA meet only at the end of a unit.
+//     The ring runs ahead across units;
+//   * scores are computed transposed, S^T = K Q^T with the tokens as the 16 rows of an
+//     mma tile and the query rows as its 8 columns, so that a group of up to eight
+//     heads wastes nothing; O^T = V^T P^T likewise.  Tensor time is far below the
+//     memory time at these row counts, which is why the warp-level mma is used: its
+//     operands are registers, where the 4-bit codes are expanded;
+//   * P is split into two 16-bit terms (two products), so that its rounding does not
+//     add to the output's own.
+//
+// 4-bit keys: the four bits of a code, masked in place out of a 32-bit word, are a
+// 16-bit float far below 1 whose value is code * 2^-133 (bf16) or code * 2^-24 (fp16),
+// 16 times that for the second code of a byte (exponents 0 and 1 have the same step, so
+// the pattern is linear in the code).  One instruction therefore expands two codes.  The
+// query rows are scaled by a power of two so that the products stay in range (those of
+// the 16 times larger codes by 2^-4 of that), and each group's product is multiplied by
+// the token's scale in fp32; zero * (sum of the query over the group) is added in fp32.
+//
+// 4-bit values: code + 16 is formed exactly in the type (an exponent or'ed to the masked
+// bits), 16 taken off, exactly, and one fused multiply-add gives scale * code + zero with
+// one rounding: the value that the read-back gives.
+#pragma once
+
+#include <type_traits>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+// ---------------------------------------------------------------------------------
+// Warp-level products and copies
+// ---------------------------------------------------------------------------------
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8).  Lane 4 g + t: A rows g, g + 8, columns
+// 2 t, 2 t + 1 (and + 8); B column g, rows 2 t, 2 t + 1 (and + 8); D rows g, g + 8,
+// columns 2 t, 2 t + 1.
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// Transpose of an 8 x 8 matrix of 16-bit values (lane 4 g + t: row g, columns 2 t, 2 t + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// 16 bytes global -> shared; only the first `bytes` (0 .. 16) are read, the rest is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* a)
+{
+    return *reinterpret_cast<const T*>(a);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if constexpr (BF16) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The codes at bits 4 P .. 4 P + 3 of both halves of a word: in place (or 8 bits up) as a
+// tiny float (see the head of the file), and as code + 16 and code.
+template <int P>
+__device__ __forceinline__ uint32_t code_tiny(uint32_t w)
+{
+    return (P >= 2 ? w >> 8 : w) & ((P & 1) ? 0x00f000f0u : 0x000f000fu);
+}
+template <bool BF16, int P>
+__device__ __forceinline__ uint32_t code_plus16(uint32_t w)
+{
+    if constexpr (BF16) {  // bits 3 .. 6 under the exponent of 16
+        const uint32_t x = P == 0 ? w << 3 : w >> (4 * P - 3);
+        return (x & 0x00780078u) | 0x41804180u;
+    } else {               // bits 6 .. 9
+        const uint32_t x = P == 0 ? w << 6 : P == 1 ? w << 2 : w >> (4 * P - 6);
+        return (x & 0x03c003c0u) | 0x4c004c00u;
+    }
+}
+
+template <bool BF16, int P>
+__device__ __forceinline__ uint32_t code_value(uint32_t w)
+{
+    return add16x2<BF16>(code_plus16<BF16, P>(w), BF16 ? 0xc180c180u : 0xcc00cc00u);
+}
+
+// ---------------------------------------------------------------------------------
+// Parameters
+// ---------------------------------------------------------------------------------
+// A unit that was cut: its pieces are slot 2 i + 1 of the CTA i that writes the record
+// and slots 2 j of the CTAs i < j <= last whose range is not empty.
+struct PagedRecord {
+    int b, u, last;  // last < 0: nothing to join
+    int pad;
+    long long total;
+};
+
+struct PagedFwdParams {
+    const void* q;
+    const void *k_cache, *v_cache;
+    void* o;
+    float* lse;
+    const int *cu_q, *seqlens_k;
+    PoolView pool;
+    int B, max_q, total_q, Hq, group, causal;
+    float sl2;         // scale * log2(e)
+    float* opart;      // [2 grid][rows of a unit][D]
+    float2* mlpart;    // [2 grid][rows of a unit] (reference maximum, sum)
+    PagedRecord* rec;  // [grid]
+};
+
+template <int D, bool INT4, int NT>
+struct PagedCfg {
+    static constexpr int TS = INT4 ? 32 : 16;      // tokens of a warp's step
+    static constexpr int MB = TS / 16;
+    static constexpr int W = INT4 && D == 128 && NT == 1 ? 8 : 4;  // warps
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int GR = W * TS;              // tokens of a granule
+    static constexpr int RB = INT4 ? D / 2 : 2 * D;  // bytes of a row (codes)
+    static constexpr int RBS = RB <= 64 ? 64 : (RB + 127) / 128 * 128;  // its pitch
+    static constexpr int SCB = INT4 ? D / 8 : 0;   // bytes of a row's (scale, zero) pairs
+    static constexpr uint32_t SLOT = TS * (RBS + SCB);
+    // slots of a warp's ring, K and V taking turns; what two CTAs per SM (one at the
+    // widest rows) leave in shared memory
+    static constexpr int CTAS = D >= (INT4 ? 384 : 256) ? 1 : 2;
+    static constexpr int ROOM = (CTAS == 1 ? 200 : 88) * 1024;
+    static constexpr int NST_ = ROOM / (W * SLOT);
+    static constexpr int NST = NST_ > 6 ? 6 : NST_;
+    static_assert(NST >= 3, "ring depth");
+    static constexpr uint32_t OFF_Q = W * NST * SLOT;            // B fragments of Q: [NT][D / 32][32 lanes][4]
+    static constexpr uint32_t OFF_QS = OFF_Q + NT * D * 16;      // sums of Q over groups: [NT][D / 32][8]
+    static constexpr uint32_t OFF_F = OFF_QS + (INT4 ? NT * D : 0);  // score factors [NT][8]
+    static constexpr uint32_t OFF_ML = OFF_F + NT * 32;          // [W][ROWS] (m, l)
+    static constexpr uint32_t OFF_OK = OFF_ML + W * ROWS * 8;    // [W][NST] blocks of a slot that have a page
+    static constexpr uint32_t OFF_RED = (OFF_OK + W * NST * 4 + 15u) & ~15u;  // [W][8][MP] a part of O
+    static constexpr int MP = 68;                                // 64 dims; pitch 4 mod 16: conflict-free
+    static constexpr uint32_t SMEM = OFF_RED + W * 8 * MP * 4;
+    static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
+    static constexpr int THREADS = W * 32;
+};
+
+// Lengths of sequence b as the kernels use them.
+struct PagedSeq {
+    int q0, Sq, Sk, nu, kt;
+};
+template <class C>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedFwdParams& p, int b)
+{
+    PagedSeq s;
+    s.q0 = p.cu_q[b];
+    const long long end = p.cu_q[b + 1];
+    s.Sq = s.q0 >= 0 && end <= p.total_q && end > s.q0 ? static_cast<int>(min(end - s.q0, static_cast<long long>(p.max_q))) : 0;
+    s.Sk = max(0, min(p.seqlens_k[b], p.pool.max_pages << p.pool.page_shift));
+    s.nu = static_cast<int>((static_cast<long long>(s.Sq) * p.group + C::ROWS - 1) / C::ROWS) * p.pool.Hkv;
+    s.kt = s.Sk > 0 ? (s.Sk - 1) / C::GR + 1 : 1;
+    return s;
+}
+
+// Sum over the block (every thread gets it); `red` holds 33 values.
+__device__ __forceinline__ long long block_sum(long long x, long long* red)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    long long s = 0;
+    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += red[i];
+    return s;
+}
+
+// Where a CTA's range of granules begins: sequence b, granule `at` of its nu * kt.
+struct PagedStart {
+    int b;
+    long long at, lo, hi, total;
+};
+template <class C>
+__device__ __forceinline__ void paged_start(const PagedFwdParams& p, PagedStart* out, long long* red)
+{
+    const int T = blockDim.x, tid = threadIdx.x;
+    long long mine = 0;
+    for (int b = tid; b < p.B; b += T) {
+        const PagedSeq s = paged_seq<C>(p, b);
+        mine += static_cast<long long>(s.nu) * s.kt;
+        if (blockIdx.x == 0 && p.seqlens_k[b] > (p.pool.max_pages << p.pool.page_shift)) record_bad_page(PAGED_FWD);
+    }
+    const long long total = block_sum(mine, red);
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) *out = PagedStart{0, 0, lo, hi, total};
+    long long before = 0;
+    for (int c = 0; c < p.B; c += T) {  // T sequences at a time: an inclusive sum over the block
+        long long x = 0;
+        if (c + tid < p.B) {
+            const PagedSeq s = paged_seq<C>(p, c + tid);
+            x = static_cast<long long>(s.nu) * s.kt;
+        }
+        const long long own = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if ((tid & 31) >= o) x += y;
+        }
+        __syncthreads();
+        if ((tid & 31) == 31) red[tid >> 5] = x;
+        __syncthreads();
+        long long sum = 0;
+        for (int i = 0; i < T / 32; ++i) {
+            if (i < tid / 32) x += red[i];
+            sum += red[i];
+        }
+        x += before;
+        if (lo < hi && x - own <= lo && lo < x) {
+            out->b = c + tid;
+            out->at = lo - (x - own);
+        }
+        before += sum;
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------------
+// A range's segments: parts of units, in order.
+// ---------------------------------------------------------------------------------
+struct PagedSegment {
+    PagedSeq s;
+    int b, u, g0, g1;
+    int r0, R;     // first row of the unit, rows of the sequence
+    int kmax;      // keys that some row of the unit sees
+};
+template <class C>
+struct PagedWalk {
+    PagedSeq s;
+    int b, u, g;
+    long long left;
+
+    __device__ void init(const PagedFwdParams& p, const PagedStart& st)
+    {
+        b = st.b;
+        left = st.hi - st.lo;
+        if (left <= 0) return;
+        s = paged_seq<C>(p, b);
+        u = static_cast<int>(st.at / s.kt);
+        g = static_cast<int>(st.at - static_cast<long long>(u) * s.kt);
+    }
+    __device__ bool next(const PagedFwdParams& p, PagedSegment& x)
+    {
+        if (left <= 0) return false;
+        while (u >= s.nu) {  // units are left, so a later sequence has them
+            if (++b >= p.B) return false;
+            u = 0;
+            s = paged_seq<C>(p, b);
+        }
+        x.s = s;
+        x.b = b;
+        x.u = u;
+        x.g0 = g;
+        x.g1 = static_cast<int>(min(static_cast<long long>(s.kt), g + left));
+        x.r0 = (u / p.pool.Hkv) * C::ROWS;
+        x.R = s.Sq * p.group;
+        x.kmax = s.Sk;
+        if (p.causal) {
+            const int last = (min(x.r0 + C::ROWS, x.R) - 1) / p.group;
+            x.kmax = max(0, min(s.Sk, last + s.Sk - s.Sq + 1));
+        }
+        left -= x.g1 - x.g0;
+        g = x.g1;
+        if (g == s.kt) {
+            g = 0;
+            ++u;
+        }
+        return true;
+    }
+};
+
+// The steps of one warp, ahead of their use: the copies.
+template <int D, bool INT4, int NT>
+struct PagedLoad {
+    using C = PagedCfg<D, INT4, NT>;
+    PagedWalk<C> walk;
+    PagedSegment seg;
+    int g;               // next granule of the segment
+    bool more;
+    // the step whose copies come next, and the one after it (its pages on their way)
+    int base[2], kmax[2], h[2], page[2];
+    uint32_t ring, ok;   // shared-memory addresses of this warp's slots and their page bits
+    uint32_t e = 0;      // copies issued (even: K, odd: V)
+
+    __device__ void init(const PagedFwdParams& p, const PagedStart& st, uint32_t ring_, uint32_t ok_)
+    {
+        ring = ring_;
+        ok = ok_;
+        walk.init(p, st);
+        more = walk.next(p, seg);
+        g = seg.g0;
+        fetch(p, 0);
+        fetch(p, 1);
+    }
+    // the warp's next step into entry i; base < 0: none is left
+    __device__ void fetch(const PagedFwdParams& p, int i)
+    {
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        base[i] = -1;
+        while (more) {
+            if (g < seg.g1) {
+                const long long first = static_cast<long long>(g) * C::GR + w * C::TS;
+                if (first < seg.kmax) {
+                    const int at = static_cast<int>(first);
+                    ++g;
+                    base[i] = at;
+                    kmax[i] = seg.kmax;
+                    h[i] = seg.u % p.pool.Hkv;
+                    const int j = at + (lane % C::MB) * 16;
+                    page[i] = j < seg.kmax
+                                  ? p.pool.table[static_cast<size_t>(seg.b) * p.pool.max_pages + (j >> p.pool.page_shift)]
+                                  : 0;
+                    return;
+                }
+            }
+            more = walk.next(p, seg);
+            g = seg.g0;
+        }
+    }
+    __device__ void issue(const PagedFwdParams& p)
+    {
+        const int lane = threadIdx.x & 31;
+        const bool value = e & 1u;
+        if (base[0] >= 0) {
+            const uint32_t n = e % C::NST;
+            const uint32_t dst = ring + n * C::SLOT;
+            const bool good = page[0] >= 0 && page[0] < p.pool.num_pages;
+            const uint32_t bits = __ballot_sync(0xffffffffu, good);
+            if (lane == 0) {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(ok + 4u * n), "r"(bits) : "memory");
+            }
+            if (!value && !good) record_bad_page(PAGED_FWD);
+#pragma unroll
+            for (int mb = 0; mb < C::MB; ++mb) {
+                const int pg = __shfl_sync(0xffffffffu, page[0], mb);
+                const bool fine = bits >> mb & 1u;
+                const int valid = fine ? min(16, kmax[0] - base[0] - mb * 16) : 0;  // tokens to read (may be <= 0)
+                const int slot0 = (base[0] + mb * 16) & (p.pool.page_size - 1);
+                const uint8_t* blk = static_cast<const uint8_t*>(value ? p.v_cache : p.k_cache) +
+                                     (fine ? pool_block<D, INT4>(p.pool, pg, h[0]) : 0);
+                const uint8_t* rows = blk + static_cast<size_t>(slot0) * C::RB;
+                constexpr int CH = C::RB / 16;  // chunks per row
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i) {
+                    const int x = lane + 32 * i, r = x / CH, c = x - r * CH, rr = mb * 16 + r;
+                    const int sw = C::RBS == 64 ? c ^ ((rr >> 1) & 3) : c ^ (rr & 7);
+                    copy16(dst + rr * C::RBS + sw * 16, rows + (r < valid ? r * C::RB + c * 16 : 0), r < valid ? 16u : 0u);
+                }
+                if constexpr (INT4) {
+                    const uint8_t* sc = blk + static_cast<size_t>(p.pool.page_size) * C::RB + static_cast<size_t>(slot0) * C::SCB;
+#pragma unroll
+                    for (int i = 0; i < (C::SCB + 31) / 32; ++i) {  // SCB chunks of 16 bytes per 16 tokens
+                        const int x = lane + 32 * i;
+                        if (x < C::SCB) {
+                            const int n = max(0, min(16, valid * C::SCB - x * 16));
+                            copy16(dst + C::TS * C::RBS + mb * 16 * C::SCB + x * 16, sc + (n > 0 ? x * 16 : 0), n);
+                        }
+                    }
+                }
+            }
+            if (value) {
+                base[0] = base[1];
+                kmax[0] = kmax[1];
+                h[0] = h[1];
+                page[0] = page[1];
+                fetch(p, 1);
+            }
+        }
+        copy_commit();
+        ++e;
+    }
+};
+
+// ---------------------------------------------------------------------------------
+// Q of a unit into shared memory, as the B fragments of the score products.
+// ---------------------------------------------------------------------------------
+template <int D, bool BF16, bool INT4, int NT>
+__device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const PagedSegment& x, uint8_t* smem)
+{
+    using C = PagedCfg<D, INT4, NT>;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
+    const int h0 = (x.u % p.pool.Hkv) * p.group;
+    for (int nt = w; nt < NT; nt += C::W) {
+        const int r = x.r0 + nt * 8 + gg;
+        const int tok = r / p.group;
+        const bool ok = r < x.R;
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                              (static_cast<size_t>(x.s.q0 + (ok ? tok : 0)) * p.Hq + h0 + (ok ? r - tok * p.group : 0)) * D;
+        uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_Q) + nt * (D / 32) * 32 + lane;
+        if constexpr (!INT4) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {  // two steps of 16 dims
+                const uint32_t* s = reinterpret_cast<const uint32_t*>(src + k * 32) + t;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (ok) v = make_uint4(s[0], s[4], s[8], s[12]);
+                dst[k * 32] = v;
+            }
+        } else {
+            // dims 8 t .. 8 t + 7 of each group: pairs (i, i + 4)
+            uint4 v[D / 32];
+            float big = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                v[k] = ok ? reinterpret_cast<const uint4*>(src + k * 32)[t] : make_uint4(0u, 0u, 0u, 0u);
+                float f[8];
+                pg_unpack8<BF16>(v[k], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[i]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // the row's power of two: its largest value comes to 2^62 (bf16) or 2^14 (fp16)
+            const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+            const int kq = BF16 ? max(7, min(100, 62 - ex)) : max(-2, min(38, 14 - ex));
+            const float up = __uint_as_float(static_cast<uint32_t>(kq + 127) << 23);
+            // the codes are 2^-133 (bf16) or 2^-24 (fp16) small
+            const int dn = (BF16 ? 133 : 24) - kq;  // 33 .. 126 or -14 .. 26
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - dn) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float f[8], sum = 0.0f;
+                pg_unpack8<BF16>(v[k], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += f[i];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (t == 0) reinterpret_cast<float*>(smem + C::OFF_QS)[(nt * (D / 32) + k) * 8 + gg] = sum * down;
+                uint32_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = (i & 1) ? up * 0.0625f : up;
+                    b[i] = pg_pack2<BF16>(f[i] * u, f[i + 4] * u);
+                }
+                dst[k * 32] = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+            // the score's factor undoes both
+            if (t == 0)
+                reinterpret_cast<float*>(smem + C::OFF_F)[nt * 8 + gg] = p.sl2 * __uint_as_float(static_cast<uint32_t>(dn + 127) << 23);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------------
+template <int D, bool BF16, bool INT4, int NT>
+__global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, INT4, NT>::CTAS)
+    fa_fwd_paged_kernel(const __grid_constant__ PagedFwdParams p)
+{
+    using C = PagedCfg<D, INT4, NT>;
+    constexpr int MB = C::MB;
+    constexpr int MT = D / 16;  // 16-dim tiles of O^T
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PagedStart start;
+    __shared__ long long red[33];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
+    const uint32_t sbase = smem_u32(smem);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    paged_start<C>(p, &start, red);
+    if (threadIdx.x == 0) p.rec[blockIdx.x].last = -1;
+    if (start.lo >= start.hi) return;
+
+    const uint32_t ring = sbase + w * C::NST * C::SLOT;
+    const uint32_t okw = sbase + C::OFF_OK + w * C::NST * 4;
+    PagedLoad<D, INT4, NT> load;
+    load.init(p, start, ring, okw);
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; ++i) load.issue(p);
+    uint32_t e = 0;  // copies consumed
+
+    // the mma row of a score tile that holds token (row & 7): at the narrowest rows the
+    // tokens are dealt so that the value loads of a warp meet no bank twice
+    auto tok_of = [](int slot) {
+        return C::RBS == 64 && INT4 ? (slot & ~3) | ((slot & 1) << 1) | ((slot >> 1) & 1) : slot;
+    };
+    const int row_a = tok_of(gg);
+
+    PagedWalk<C> walk;
+    walk.init(p, start);
+    PagedSegment x;
+    while (walk.next(p, x)) {
+        __syncthreads();  // the last unit's Q and partial sums are done with
+        paged_stage_q<D, BF16, INT4, NT>(p, x, smem);
+        __syncthreads();
+
+        float o[MT][NT][4];
+        float m[NT][2], l[NT][2], f[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[nt][i] = -INFINITY;
+                l[nt][i] = 0.0f;
+                const int r = x.r0 + nt * 8 + 2 * t + i;
+                f[nt][i] = INT4 ? reinterpret_cast<const float*>(smem + C::OFF_F)[nt * 8 + 2 * t + i] : p.sl2;
+                lim[nt][i] = p.causal && r < x.R ? min(x.s.Sk, r / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;
+            }
+        }
+        const int lim0 = p.causal ? min(x.s.Sk, x.r0 / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;  // the least
+
+        for (int g = x.g0; g < x.g1; ++g) {
+            if (static_cast<long long>(g) * C::GR + w * C::TS >= x.kmax) break;
+            const int base = g * C::GR + w * C::TS;
+            // ---- scores
+            copy_wait<C::NST - 2>();
+            __syncwarp();
+            load.issue(p);  // into the slot consumed last
+            const uint32_t at = (w * C::NST + e % C::NST) * C::SLOT;  // offset of the slot
+            const uint8_t* const ks = smem + at;
+            const uint32_t bits = lds<uint32_t>(smem + C::OFF_OK + (w * C::NST + e % C::NST) * 4);
+            ++e;
+            float s[MB][NT][4];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[mb][nt][i] = 0.0f;
+            if constexpr (!INT4) {
+                const int r = lane & 15;
+                const uint32_t row = sbase + at + r * C::RBS;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t a0[4], a1[4];
+                    const int c = 4 * k + (lane >> 4);
+                    ldmatrix4(a0, row + ((c ^ (r & 7)) << 4));
+                    ldmatrix4(a1, row + (((c + 2) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 b = lds<uint4>(smem + C::OFF_Q + ((nt * (D / 32) + k) * 32 + lane) * 16);
+                        mma16816<BF16>(s[0][nt], a0, b.x, b.y);
+                        mma16816<BF16>(s[0][nt], a1, b.z, b.w);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k4 = 0; k4 < D / 32; k4 += (D % 128 == 0 ? 4 : 2)) {
+                    constexpr int KG = D % 128 == 0 ? 4 : 2;  // groups per load of pairs
+                    uint32_t pr[MB][2][KG];
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint8_t* a = ks + C::TS * C::RBS + (mb * 16 + y * 8 + row_a) * C::SCB + k4 * 4;
+                            if constexpr (KG == 4) {
+                                const uint4 v = lds<uint4>(a);
+                                pr[mb][y][0] = v.x;
+                                pr[mb][y][1] = v.y;
+                                pr[mb][y][2] = v.z;
+                                pr[mb][y][3] = v.w;
+                            } else {
+                                const uint2 v = lds<uint2>(a);
+                                pr[mb][y][0] = v.x;
+                                pr[mb][y][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                    for (int kk = 0; kk < KG; ++kk) {
+                        const int k = k4 + kk;
+                        uint4 b[NT];
+                        float2 qs[NT];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            b[nt] = lds<uint4>(smem + C::OFF_Q + ((nt * (D / 32) + k) * 32 + lane) * 16);
+                            qs[nt] = lds<float2>(smem + C::OFF_QS + ((nt * (D / 32) + k) * 8 + 2 * t) * 4);
+                        }
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) {
+                            const int ra = mb * 16 + row_a, rb = ra + 8;
+                            const int ca = C::RBS == 64 ? k ^ ((ra >> 1) & 3) : k ^ (ra & 7);
+                            const int cb = C::RBS == 64 ? k ^ ((rb >> 1) & 3) : k ^ (rb & 7);
+                            const uint32_t wa = lds<uint32_t>(ks + ra * C::RBS + ca * 16 + t * 4);
+                            const uint32_t wb = lds<uint32_t>(ks + rb * C::RBS + cb * 16 + t * 4);
+                            const uint32_t a0[4] = {code_tiny<0>(wa), code_tiny<0>(wb), code_tiny<1>(wa), code_tiny<1>(wb)};
+                            const uint32_t a1[4] = {code_tiny<2>(wa), code_tiny<2>(wb), code_tiny<3>(wa), code_tiny<3>(wb)};
+                            const float2 za = pg_unpack2<BF16>(pr[mb][0][kk]), zb = pg_unpack2<BF16>(pr[mb][1][kk]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816<BF16>(d, a0, b[nt].x, b[nt].y);
+                                mma16816<BF16>(d, a1, b[nt].z, b[nt].w);
+                                s[mb][nt][0] = fmaf(za.x, d[0], fmaf(za.y, qs[nt].x, s[mb][nt][0]));
+                                s[mb][nt][1] = fmaf(za.x, d[1], fmaf(za.y, qs[nt].y, s[mb][nt][1]));
+                                s[mb][nt][2] = fmaf(zb.x, d[2], fmaf(zb.y, qs[nt].x, s[mb][nt][2]));
+                                s[mb][nt][3] = fmaf(zb.x, d[3], fmaf(zb.y, qs[nt].y, s[mb][nt][3]));
+                            }
+                        }
+                    }
+                }
+            }
+            // ---- masks: causal limits, the sequence's end, tokens without a page
+            const bool whole = (bits & ((1u << MB) - 1u)) == (1u << MB) - 1u;
+            if (base > lim0 - C::TS || !whole) {
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j = base + mb * 16 + y * 8 + row_a;
+                        const bool has = bits >> mb & 1u;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!has || j >= lim[nt][i]) s[mb][nt][2 * y + i] = -INFINITY;
+                    }
+            }
+            // ---- online softmax; columns 2 t, 2 t + 1 of each tile
+            bool grow = false;
+            float mx[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float v = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
+                    if constexpr (MB == 2) v = fmaxf(v, fmaxf(s[1][nt][i], s[1][nt][2 + i]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mx[nt][i] = v * f[nt][i];
+                    grow |= mx[nt][i] > m[nt][i] + 8.0f;
+                }
+            // the reference maximum moves (and O and l with it) only when a score exceeds it
+            // by more than 2^8: until then the weights stay far inside the types' range
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float al[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mn = fmaxf(m[nt][i], mx[nt][i]);
+                        al[i] = m[nt][i] == mn ? 1.0f : ex2_sfu(m[nt][i] - mn);
+                        m[nt][i] = mn;
+                        l[nt][i] *= al[i];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[mt][nt][i] *= al[i & 1];
+                }
+            }
+            // ---- P, in two 16-bit terms, as the B fragments of the second product
+            uint32_t ph[MB][NT][2], pl[MB][NT][2];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float v[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float ref = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+                            v[i] = ex2_sfu(fmaf(s[mb][nt][2 * y + i], f[nt][i], -ref));
+                            l[nt][i] += v[i];
+                        }
+                        const uint32_t hi = pg_pack2<BF16>(v[0], v[1]);
+                        const float2 b = pg_unpack2<BF16>(hi);
+                        ph[mb][nt][y] = transpose8x8(hi);
+                        pl[mb][nt][y] = transpose8x8(pg_pack2<BF16>(v[0] - b.x, v[1] - b.y));
+                    }
+            // ---- O^T += V^T P^T
+            copy_wait<C::NST - 2>();
+            __syncwarp();
+            load.issue(p);
+            const uint32_t vat = (w * C::NST + e % C::NST) * C::SLOT;
+            const uint8_t* const vs = smem + vat;
+            ++e;
+            if constexpr (!INT4) {
+                const int r = (lane & 7) + ((lane >> 4) << 3);
+                const uint32_t row = sbase + vat + r * C::RBS;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t a[4];
+                    ldmatrix4_trans(a, row + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816<BF16>(o[mt][nt], a, ph[0][nt][0], ph[0][nt][1]);
+                        mma16816<BF16>(o[mt][nt], a, pl[0][nt][0], pl[0][nt][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    const int tk[4] = {mb * 16 + tok_of(2 * t), mb * 16 + tok_of(2 * t + 1), mb * 16 + tok_of(2 * t + 8),
+                                       mb * 16 + tok_of(2 * t + 9)};
+#pragma unroll
+                    for (int ws = 0; ws < D / 64; ++ws) {  // 64 dims: word gg of eight
+                        uint32_t wd[4], pr[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = 2 * ws + (gg >> 2);
+                            const int sw = C::RBS == 64 ? c ^ ((tk[i] >> 1) & 3) : c ^ (tk[i] & 7);
+                            wd[i] = lds<uint32_t>(vs + tk[i] * C::RBS + sw * 16 + (gg & 3) * 4);
+                            pr[i] = lds<uint32_t>(vs + C::TS * C::RBS + tk[i] * C::SCB + c * 4);
+                        }
+                        const uint32_t lo01 = __byte_perm(wd[0], wd[1], 0x5410), hi01 = __byte_perm(wd[0], wd[1], 0x7632);
+                        const uint32_t lo23 = __byte_perm(wd[2], wd[3], 0x5410), hi23 = __byte_perm(wd[2], wd[3], 0x7632);
+                        const uint32_t s01 = __byte_perm(pr[0], pr[1], 0x5410), z01 = __byte_perm(pr[0], pr[1], 0x7632);
+                        const uint32_t s23 = __byte_perm(pr[2], pr[3], 0x5410), z23 = __byte_perm(pr[2], pr[3], 0x7632);
+                        auto tile = [&](auto P) {
+                            constexpr int j = decltype(P)::value;
+                            const uint32_t a[4] = {fma16x2<BF16>(code_value<BF16, j>(lo01), s01, z01),
+                                                   fma16x2<BF16>(code_value<BF16, j>(hi01), s01, z01),
+                                                   fma16x2<BF16>(code_value<BF16, j>(lo23), s23, z23),
+                                                   fma16x2<BF16>(code_value<BF16, j>(hi23), s23, z23)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<BF16>(o[ws * 4 + j][nt], a, ph[mb][nt][0], ph[mb][nt][1]);
+                                mma16816<BF16>(o[ws * 4 + j][nt], a, pl[mb][nt][0], pl[mb][nt][1]);
+                            }
+                        };
+                        tile(std::integral_constant<int, 0>{});
+                        tile(std::integral_constant<int, 1>{});
+                        tile(std::integral_constant<int, 2>{});
+                        tile(std::integral_constant<int, 3>{});
+                    }
+                }
+            }
+        }
+
+        // ---- the warps' pieces of the unit become one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = l[nt][i];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (gg == 0)
+                    reinterpret_cast<float2*>(smem + C::OFF_ML)[w * C::ROWS + nt * 8 + 2 * t + i] = make_float2(m[nt][i], v);
+            }
+        __syncthreads();
+        const float2* ml = reinterpret_cast<const float2*>(smem + C::OFF_ML);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < C::W; ++v) top = fmaxf(top, ml[v * C::ROWS + nt * 8 + 2 * t + i].x);
+                const float al = m[nt][i] == -INFINITY ? 0.0f : ex2_sfu(m[nt][i] - top);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][nt][i] *= al;
+                    o[mt][nt][2 + i] *= al;
+                }
+            }
+        const bool whole = x.g0 == 0 && x.g1 == x.s.kt;
+        const size_t piece = (2 * static_cast<size_t>(blockIdx.x) + (x.g0 == 0 ? 1 : 0)) * C::ROWS;
+        const int h0 = (x.u % p.pool.Hkv) * p.group;
+        float* buf = reinterpret_cast<float*>(smem + C::OFF_RED);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int part = 0; part < D / 64; ++part) {
+                if (nt + part > 0) __syncthreads();
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        buf[(w * 8 + 2 * t + (i & 1)) * C::MP + y * 16 + (i >> 1) * 8 + gg] = o[part * 4 + y][nt][i];
+                __syncthreads();
+                // thread: row rr of the tile, eight neighbouring dims (word v of the part)
+                for (int y = threadIdx.x; y < 64; y += C::THREADS) {
+                    const int rr = y >> 3, v = y & 7, r = x.r0 + nt * 8 + rr;
+                    if (r >= x.R) continue;
+                    float acc[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll
+                    for (int ww = 0; ww < C::W; ++ww)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            // place of dim 8 v + i of the part in the tiles
+                            const int at = INT4 ? (i & 3) * 16 + (i >> 2) * 8 + v : 8 * v + i;
+                            acc[i] += buf[(ww * 8 + rr) * C::MP + at];
+                        }
+                    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int ww = 0; ww < C::W; ++ww) top = fmaxf(top, ml[ww * C::ROWS + nt * 8 + rr].x);
+#pragma unroll
+                    for (int ww = 0; ww < C::W; ++ww) {
+                        const float2 z = ml[ww * C::ROWS + nt * 8 + rr];
+                        if (z.x != -INFINITY) sum += z.y * ex2_sfu(z.x - top);
+                    }
+                    if (whole) {
+                        const int tok = r / p.group, h = h0 + r - tok * p.group;
+                        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[i] *= inv;
+                        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
+                                                 (static_cast<size_t>(x.s.q0 + tok) * p.Hq + h) * D + part * 64)[v] =
+                            pg_pack8<BF16>(acc);
+                        if (part == 0 && v == 0)
+                            p.lse[static_cast<size_t>(h) * p.total_q + x.s.q0 + tok] =
+                                sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.opart + (piece + nt * 8 + rr) * D + part * 64 + v * 8);
+                        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                        if (part == 0 && v == 0) p.mlpart[piece + nt * 8 + rr] = make_float2(top, sum);
+                    }
+                }
+            }
+        }
+        if (!whole && x.g0 == 0 && threadIdx.x == 0) {
+            // the pieces that follow are in the ranges up to the one that holds the unit's end
+            const long long end = start.hi + (x.s.kt - x.g1);
+            const long long last = (end * gridDim.x + start.total - 1) / start.total - 1;
+            p.rec[blockIdx.x] = PagedRecord{x.b, x.u, static_cast<int>(last), 0, start.total};
+        }
+    }
+    copy_wait<0>();
+}
+
+// ---------------------------------------------------------------------------------
+// Joins the pieces of the units that were cut: one block per (record, row), its warps
+// taking the pieces in turn; the order of every sum is fixed.
+// ---------------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+template <int D, bool BF16, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(const __grid_constant__ PagedFwdParams p, int grid)
+{
+    __shared__ float part[kJoinWarps][D];
+    __shared__ float2 ml[kJoinWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedRecord rec = p.rec[blockIdx.x];
+    if (rec.last < 0) return;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q0 = p.cu_q[rec.b];
+    const int Sq = max(0, min(p.cu_q[rec.b + 1] - q0, p.max_q));
+    const int r = (rec.u / p.pool.Hkv) * ROWS + blockIdx.y;
+    if (r >= Sq * p.group) return;
+    constexpr int PER = D / 32;
+    float acc[PER], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = 0.0f;
+    for (int j = blockIdx.x + w; j <= rec.last; j += kJoinWarps) {
+        if (rec.total * j / grid == rec.total * (j + 1) / grid) continue;  // an empty range
+        const size_t piece = (2 * static_cast<size_t>(j) + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * ROWS + blockIdx.y;
+        const float2 z = p.mlpart[piece];
+        if (z.x == -INFINITY) continue;
+        const float mn = fmaxf(m, z.x), a = ex2_sfu(m - mn), b = ex2_sfu(z.x - mn);
+        m = mn;
+        l = l * a + z.y * b;
+        const float* src = p.opart + piece * D + lane;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) acc[c] = acc[c] * a + src[32 * c] * b;
+    }
+#pragma unroll
+    for (int c = 0; c < PER; ++c) part[w][lane + 32 * c] = acc[c];
+    if (lane == 0) ml[w] = make_float2(m, l);
+    __syncthreads();
+    float top = -INFINITY, sum = 0.0f, f[kJoinWarps];
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+        f[i] = ml[i].x == -INFINITY ? 0.0f : ex2_sfu(ml[i].x - top);
+        sum += ml[i].y * f[i];
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int tok = r / p.group, h = (rec.u % p.pool.Hkv) * p.group + r - tok * p.group;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (static_cast<size_t>(q0 + tok) * p.Hq + h) * D);
+    for (int c = threadIdx.x; c < D / 2; c += kJoinWarps * 32) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            a = fmaf(f[i], part[i][2 * c], a);
+            b = fmaf(f[i], part[i][2 * c + 1], b);
+        }
+        dst[c] = pg_pack2<BF16>(a * inv, b * inv);
+    }
+    if (threadIdx.x == 0)
+        p.lse[static_cast<size_t>(h) * p.total_q + q0 + tok] =
+            sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace fa
