@@ -66,7 +66,9 @@ def _stream_ptr(stream) -> int:
     """The stream handle to launch on: the given one, else the current device's current
     stream (the wrappers make q's device current first)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -331,47 +333,67 @@ def fa_kv_cache_size(num_pages: int, page_size: int, Hkv: int, d: int, fmt: int 
     return int(_lib.load().fa_kv_cache_size(num_pages, page_size, Hkv, d, fmt))
 
 
-def _check_cache(k_cache, v_cache, dtype, block_table, ref, **index):
-    """Validates a pair of pools and the int32 index arrays of a paged-cache call; returns
-    (num_pages, Hkv, page_size, d, fmt, B, max_pages).  Pools are [num_pages, Hkv,
-    page_size, d] in the call's dtype, or uint8 [num_pages, Hkv, page_size, 5 d / 8]."""
-    _check(k_cache, "k_cache")
-    _check(v_cache, "v_cache", k_cache.dtype)
-    int4 = k_cache.dtype == torch.uint8
-    if not int4 and k_cache.dtype != dtype:
-        raise ValueError(f"fa: k_cache has dtype {k_cache.dtype}, expected {dtype} or uint8")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+class _Here:
+    """Stands for torch.cuda.device(...) where that device is current already: the paged
+    calls are a few microseconds on the GPU, and switching costs as much on the host."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device):
+    return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
+def _check_index(t, name, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"fa: {name} must be a contiguous int32 tensor on {device}")
+    if t.shape != shape:
+        raise ValueError(f"fa: {name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _check_cache(k_cache, v_cache, dtype, block_table, device):
+    """Validates a pair of pools and their block table; returns (num_pages, Hkv,
+    page_size, d, fmt, B, max_pages).  Pools are [num_pages, Hkv, page_size, d] in the
+    call's dtype, or uint8 [num_pages, Hkv, page_size, 5 d / 8]."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+            raise ValueError(f"fa: {name} must be a contiguous tensor on {device}")
+    shape, kind = k_cache.shape, k_cache.dtype
+    if kind != v_cache.dtype or (kind != dtype and kind != torch.uint8):
+        raise ValueError(f"fa: the pools have dtypes {kind} and {v_cache.dtype}, expected {dtype} or uint8")
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("fa: k_cache and v_cache must be [num_pages, Hkv, page_size, d] (4-bit: 5 d / 8 bytes)")
-    num_pages, Hkv, page_size, width = k_cache.shape
-    if int4 and width % 5:
-        raise ValueError(f"fa: a 4-bit pool has 5 d / 8 bytes per token, got {width}")
+    num_pages, Hkv, page_size, width = shape
+    fmt = FA_KV_16
+    if kind == torch.uint8:
+        if width % 5:
+            raise ValueError(f"fa: a 4-bit pool has 5 d / 8 bytes per token, got {width}")
+        width, fmt = width * 8 // 5, FA_KV_INT4
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("fa: block_table must be a [B, max_pages] tensor")
     B, max_pages = block_table.shape
-    for name, t, n in (("block_table", block_table, None), ("seqlens_k", index.get("seqlens_k"), B),
-                       (index["cu_name"], index["cu"], B + 1)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.device != ref.device or t.dtype != torch.int32 or \
-                not t.is_contiguous():
-            raise ValueError(f"fa: {name} must be a contiguous int32 tensor on {ref.device}")
-        if n is not None and t.shape != (n,):
-            raise ValueError(f"fa: {name} has shape {tuple(t.shape)}, expected ({n},)")
-    _same_device(ref, k_cache=k_cache, v_cache=v_cache)
-    return (num_pages, Hkv, page_size, width * 8 // 5 if int4 else width, FA_KV_INT4 if int4 else FA_KV_16, B,
-            max_pages)
+    _check_index(block_table, "block_table", (B, max_pages), device)
+    return num_pages, Hkv, page_size, width, fmt, B, max_pages
 
 
-def _token_rows(t, name, H, d):
+def _token_rows(t, name, total, H, d, dtype, device):
     """A packed [total, H, d] tensor whose rows may lie apart (a slice of a fused
     projection); returns the distance between rows in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"fa: {name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1:] != (H, d):
-        raise ValueError(f"fa: {name} has shape {tuple(t.shape)}, expected (total, {H}, {d})")
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"fa: {name} must be a tensor on {device}")
+    if t.shape != (total, H, d) or t.dtype != dtype:
+        raise ValueError(f"fa: {name} is {tuple(t.shape)} of {t.dtype}, expected {(total, H, d)} of {dtype}")
+    row, head, one = t.stride()
+    if one != 1 or (H > 1 and head != d):
         raise ValueError(f"fa: the heads of a row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else H * d
+    return row if total > 1 else H * d
 
 
 def fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, inv_freq=None,
@@ -382,39 +404,39 @@ def fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, 
     the new tokens per sequence; seqlens_k [B]: its cached tokens, the new ones included;
     block_table [B,max_pages].  q, k, v may be slices of a fused projection.  q may be
     None.  Returns the rotated q [total,Hq,d]."""
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("fa: k must be [total, Hkv, d]")
-    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(
-        k_cache, v_cache, k.dtype, block_table, k, seqlens_k=seqlens_k, cu_name="cu_seqlens", cu=cu_seqlens)
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("fa: k must be a CUDA tensor [total, Hkv, d]")
+    device, dtype, total = k.device, k.dtype, k.shape[0]
     dt = _dtype_code(k)
-    k_stride, v_stride = _token_rows(k, "k", Hkv, d), _token_rows(v, "v", Hkv, d)
-    total = k.shape[0]
+    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(k_cache, v_cache, dtype, block_table, device)
+    _check_index(cu_seqlens, "cu_seqlens", (B + 1,), device)
+    _check_index(seqlens_k, "seqlens_k", (B,), device)
+    k_stride = _token_rows(k, "k", total, Hkv, d, dtype, device)
+    v_stride = _token_rows(v, "v", total, Hkv, d, dtype, device)
     Hq, q_stride = Hkv, Hkv * d
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("fa: q must be [total, Hq, d]")
         Hq = q.shape[1]
-        q_stride = _token_rows(q, "q", Hq, d)
+        q_stride = _token_rows(q, "q", total, Hq, d, dtype, device)
         if q_out is None:
-            q_out = torch.empty(total, Hq, d, dtype=q.dtype, device=q.device)
-        _check(q_out, "q_out", k.dtype)
-        _shape(q_out, "q_out", (total, Hq, d))
+            q_out = torch.empty((total, Hq, d), dtype=dtype, device=device)
+        else:
+            _check(q_out, "q_out", dtype)
+            _shape(q_out, "q_out", (total, Hq, d))
     elif q_out is not None:
         raise ValueError("fa: q_out without q")
-    for name, t in (("q", q), ("v", v)):
-        if t is not None and (t.dtype != k.dtype or t.shape[0] != total):
-            raise ValueError(f"fa: {name} has {t.shape[0]} rows of {t.dtype}, expected {total} of {k.dtype}")
     rot = 0
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", torch.float32)
         rot = 2 * inv_freq.numel()
-    _same_device(k, q=q, v=v, q_out=q_out, inv_freq=inv_freq)
-    with torch.cuda.device(k.device):
+    _same_device(k, q_out=q_out, inv_freq=inv_freq)
+    with _on(device):
         code = _lib.load().fa_kv_append(
             q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
             q_out.data_ptr() if q is not None else None, k_cache.data_ptr(), v_cache.data_ptr(),
             cu_seqlens.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(),
-            inv_freq.data_ptr() if rot else None, rot, int(bool(interleaved)), B, total, Hq, Hkv, d, page_size,
+            inv_freq.data_ptr() if rot else None, rot, 1 if interleaved else 0, B, total, Hq, Hkv, d, page_size,
             num_pages, max_pages, fmt, dt, _stream_ptr(stream))
     _raise(code, "fa_kv_append")
     return q_out
@@ -430,18 +452,19 @@ def fa_kv_gather(k_cache, v_cache, cu_seqlens_k, block_table, total_k: int, dtyp
         dtype = k_cache.dtype if dtype is None else dtype
     elif dtype is None:
         raise ValueError("fa: a 4-bit pool needs the dtype of its scales")
-    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(
-        k_cache, v_cache, dtype, block_table, k_cache, cu_name="cu_seqlens_k", cu=cu_seqlens_k)
+    device = k_cache.device
+    num_pages, Hkv, page_size, d, fmt, B, max_pages = _check_cache(k_cache, v_cache, dtype, block_table, device)
+    _check_index(cu_seqlens_k, "cu_seqlens_k", (B + 1,), device)
     total_k = int(total_k)
     shape = (total_k, Hkv, d)
-    k = torch.empty(shape, dtype=dtype, device=k_cache.device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=k_cache.device) if v is None else v
+    k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=device) if v is None else v
     dt = _dtype_code(k)
     for name, t in (("k", k), ("v", v)):
         _check(t, name, dtype)
         _shape(t, name, shape)
     _same_device(k_cache, k=k, v=v)
-    with torch.cuda.device(k_cache.device):
+    with _on(device):
         code = _lib.load().fa_kv_gather(k_cache.data_ptr(), v_cache.data_ptr(), k.data_ptr(), v.data_ptr(),
                                         cu_seqlens_k.data_ptr(), block_table.data_ptr(), B, total_k, Hkv, d,
                                         page_size, num_pages, max_pages, fmt, dt, _stream_ptr(stream))
@@ -463,28 +486,33 @@ def fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_
     if q.dim() != 3:
         raise ValueError("fa: q must be [total_q, Hq, d]")
     total_q, Hq, d = q.shape
-    num_pages, Hkv, page_size, dk, fmt, B, max_pages = _check_cache(
-        k_cache, v_cache, q.dtype, block_table, q, seqlens_k=seqlens_k, cu_name="cu_seqlens_q", cu=cu_seqlens_q)
+    device, dtype, max_seqlen_q = q.device, q.dtype, int(max_seqlen_q)
+    dt = _dtype_code(q)
+    num_pages, Hkv, page_size, dk, fmt, B, max_pages = _check_cache(k_cache, v_cache, dtype, block_table, device)
+    _check_index(cu_seqlens_q, "cu_seqlens_q", (B + 1,), device)
+    _check_index(seqlens_k, "seqlens_k", (B,), device)
     if dk != d:
         raise ValueError(f"fa: the pools hold head_dim {dk}, q has {d}")
-    dt = _dtype_code(q)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = torch.empty_like(q) if out is None else out
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", dtype)
+        _shape(out, "out", q.shape)
     if lse is None:
-        lse = torch.empty(Hq, total_q, dtype=torch.float32, device=q.device)
-    _check(out, "out", q.dtype)
-    _check(lse, "lse", torch.float32)
-    _shape(out, "out", q.shape)
-    _shape(lse, "lse", (Hq, total_q))
+        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=device)
+    else:
+        _check(lse, "lse", torch.float32)
+        _shape(lse, "lse", (Hq, total_q))
     _same_device(q, out=out, lse=lse)
     lib = _lib.load()
-    with torch.cuda.device(q.device):
-        workspace = _workspace(workspace, q, int(lib.fa_fwd_paged_workspace_size(B, int(max_seqlen_q), Hq, Hkv, d)))
+    with _on(device):
+        workspace = _workspace(workspace, q, lib.fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d))
         code = lib.fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                 lse.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
-                                block_table.data_ptr(), B, int(max_seqlen_q), total_q, Hq, Hkv, d, page_size,
-                                num_pages, max_pages, fmt, int(bool(causal)), float(scale), dt,
+                                block_table.data_ptr(), B, max_seqlen_q, total_q, Hq, Hkv, d, page_size,
+                                num_pages, max_pages, fmt, 1 if causal else 0, float(scale), dt,
                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                 _stream_ptr(stream))
     _raise(code, "fa_fwd_paged")

@@ -59,6 +59,8 @@ def load() -> ctypes.CDLL:
     """Load libfa.so from the package directory.  Raises if it is missing: there is
     no other implementation to fall back to."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

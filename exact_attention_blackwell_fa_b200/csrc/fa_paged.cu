@@ -1,6 +1,7 @@
 // fa_paged.cu -- the paged-cache entry points declared in include/fa.h: argument checks
 // and launches.  Every entry point validates first and launches nothing on an invalid
 // argument.
+#include <atomic>
 #include <cmath>
 
 #include "fa_host.h"
@@ -113,8 +114,16 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
 {
     using C = fa::PagedCfg<D, INT4, NT>;
     auto kernel = fa::fa_fwd_paged_kernel<D, BF16, INT4, NT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return FA_ERR_CUDA;
+    // once per device: the call is a noticeable part of a decode step's host time
+    static std::atomic<uint64_t> ready{0};
+    static_assert(fa::kMaxDevices <= 64, "one bit per device");
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fa::kMaxDevices) return FA_ERR_CUDA;
+    if (!(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+            return FA_ERR_CUDA;
+        ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
     // no more CTAs than there can be granules
     const long long blocks = (static_cast<long long>(p.max_q) * p.group + C::ROWS - 1) / C::ROWS;
     const long long keys = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
@@ -302,6 +311,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     p.causal = causal ? 1 : 0;
     p.sl2 = scale * 1.4426950408889634f;
     const bool bf16 = dt == FA_BF16, int4 = fmt == FA_KV_INT4;
+    p.block_bytes = static_cast<uint32_t>(page_size) * (int4 ? 5 * d / 8 : 2 * d);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (d) {
     case 128: return launch_paged_rows<128>(p, nt, bf16, int4, di.sm_count, s);

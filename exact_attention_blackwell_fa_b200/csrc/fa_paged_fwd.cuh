@@ -33,9 +33,10 @@
 // the 16 times larger codes by 2^-4 of that), and each group's product is multiplied by
 // the token's scale in fp32; zero * (sum of the query over the group) is added in fp32.
 //
-// 4-bit values: code + 16 is formed exactly in the type (an exponent or'ed to the masked
-// bits), 16 taken off, exactly, and one fused multiply-add gives scale * code + zero with
-// one rounding: the value that the read-back gives.
+// 4-bit values: a code becomes a whole number of the type exactly (its bits under the
+// exponent whose step is 1, that power of two taken off; or the tiny float multiplied
+// up), and one fused multiply-add gives scale * code + zero with one rounding: the value
+// that the read-back gives.
 #pragma once
 
 #include <type_traits>
@@ -62,6 +63,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// D = A B
+template <bool BF16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -81,8 +95,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// 16 bytes global -> shared; only the first `bytes` (0 .. 16) are read, the rest is zero.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes)
+// 16 bytes global -> shared; of the second form only the first `bytes` (0 .. 16) are
+// read, the rest is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
                  "r"(bytes)
@@ -116,30 +135,31 @@ __device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b)
     else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
-// The codes at bits 4 P .. 4 P + 3 of both halves of a word: in place (or 8 bits up) as a
-// tiny float (see the head of the file), and as code + 16 and code.
-template <int P>
+// Codes in a 32-bit word, in bits 0 .. 3 (HIGH: 4 .. 7) of both halves.
+template <bool HIGH>
 __device__ __forceinline__ uint32_t code_tiny(uint32_t w)
 {
-    return (P >= 2 ? w >> 8 : w) & ((P & 1) ? 0x00f000f0u : 0x000f000fu);
+    return w & (HIGH ? 0x00f000f0u : 0x000f000fu);
 }
-template <bool BF16, int P>
-__device__ __forceinline__ uint32_t code_plus16(uint32_t w)
+// scale * code + zero of a pair.  s4: 4 scale (bf16).
+template <bool BF16, bool HIGH>
+__device__ __forceinline__ uint32_t code_value(uint32_t w, uint32_t s, uint32_t s4, uint32_t z)
 {
-    if constexpr (BF16) {  // bits 3 .. 6 under the exponent of 16
-        const uint32_t x = P == 0 ? w << 3 : w >> (4 * P - 3);
-        return (x & 0x00780078u) | 0x41804180u;
-    } else {               // bits 6 .. 9
-        const uint32_t x = P == 0 ? w << 6 : P == 1 ? w << 2 : w >> (4 * P - 6);
-        return (x & 0x03c003c0u) | 0x4c004c00u;
-    }
-}
-
-template <bool BF16, int P>
-__device__ __forceinline__ uint32_t code_value(uint32_t w)
-{
-    return add16x2<BF16>(code_plus16<BF16, P>(w), BF16 ? 0xc180c180u : 0xcc00cc00u);
+    if constexpr (BF16 && HIGH)  // 2^-129 code, times 2^127
+        return fma16x2<true>(mul_bf16x2(w & 0x00f000f0u, 0x7f007f00u), s4, z);
+    else if constexpr (BF16)     // 128 + code
+        return fma16x2<true>(add16x2<true>((w & 0x000f000fu) | 0x43004300u, 0xc300c300u), s, z);
+    else if constexpr (HIGH)     // 64 + code
+        return fma16x2<false>(add16x2<false>((w & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s, z);
+    else                         // 1024 + code
+        return fma16x2<false>(add16x2<false>((w & 0x000f000fu) | 0x64006400u, 0xe400e400u), s, z);
 }
 
 // ---------------------------------------------------------------------------------
@@ -162,6 +182,7 @@ struct PagedFwdParams {
     PoolView pool;
     int B, max_q, total_q, Hq, group, causal;
     float sl2;         // scale * log2(e)
+    uint32_t block_bytes;  // of a (page, head)
     float* opart;      // [2 grid][rows of a unit][D]
     float2* mlpart;    // [2 grid][rows of a unit] (reference maximum, sum)
     PagedRecord* rec;  // [grid]
@@ -195,6 +216,10 @@ struct PagedCfg {
     static constexpr uint32_t SMEM = OFF_RED + W * 8 * MP * 4;
     static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
     static constexpr int THREADS = W * 32;
+    // 16-byte chunk c of row r lies at chunk c ^ key(r) of its 64- or 128-byte line, so
+    // that the fragment loads of a warp meet no bank twice
+    static constexpr int LINE = RBS == 64 ? 3 : 7;
+    __device__ static constexpr int key(int r) { return RBS == 64 ? (r >> 1) & 3 : r & 7; }
 };
 
 // Lengths of sequence b as the kernels use them.
@@ -330,28 +355,39 @@ struct PagedWalk {
     }
 };
 
-// The steps of one warp, ahead of their use: the copies.
+// The steps of one warp, ahead of their use: the copies.  K and V take turns in the ring.
 template <int D, bool INT4, int NT>
 struct PagedLoad {
     using C = PagedCfg<D, INT4, NT>;
     PagedWalk<C> walk;
     PagedSegment seg;
-    int g;               // next granule of the segment
+    const int* table;    // the segment's pages
+    int g, h;            // next granule and KV head of the segment
     bool more;
-    // the step whose copies come next, and the one after it (its pages on their way)
-    int base[2], kmax[2], h[2], page[2];
-    uint32_t ring, ok;   // shared-memory addresses of this warp's slots and their page bits
-    uint32_t e = 0;      // copies issued (even: K, odd: V)
+    // the step whose copies come next, and the one after it (its pages on their way):
+    // its first token, keys that count, KV head, page of the lane's block of 16 tokens
+    int base[2], kmax[2], hkv[2], page[2];
+    long long off[C::MB];  // of the next step's blocks in the pools
+    uint32_t bits;         // which of them have a page
+    uint32_t slot, ok;     // shared-memory addresses of this warp's next slot and its page bits
+    uint32_t n = 0;        // slot
 
     __device__ void init(const PagedFwdParams& p, const PagedStart& st, uint32_t ring_, uint32_t ok_)
     {
-        ring = ring_;
+        slot = ring_;
         ok = ok_;
         walk.init(p, st);
-        more = walk.next(p, seg);
-        g = seg.g0;
+        segment(p);
         fetch(p, 0);
         fetch(p, 1);
+    }
+    __device__ void segment(const PagedFwdParams& p)
+    {
+        more = walk.next(p, seg);
+        if (!more) return;
+        g = seg.g0;
+        h = seg.u % p.pool.Hkv;
+        table = p.pool.table + static_cast<size_t>(seg.b) * p.pool.max_pages;
     }
     // the warp's next step into entry i; base < 0: none is left
     __device__ void fetch(const PagedFwdParams& p, int i)
@@ -359,76 +395,100 @@ struct PagedLoad {
         const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
         base[i] = -1;
         while (more) {
-            if (g < seg.g1) {
-                const long long first = static_cast<long long>(g) * C::GR + w * C::TS;
-                if (first < seg.kmax) {
-                    const int at = static_cast<int>(first);
-                    ++g;
-                    base[i] = at;
-                    kmax[i] = seg.kmax;
-                    h[i] = seg.u % p.pool.Hkv;
-                    const int j = at + (lane % C::MB) * 16;
-                    page[i] = j < seg.kmax
-                                  ? p.pool.table[static_cast<size_t>(seg.b) * p.pool.max_pages + (j >> p.pool.page_shift)]
-                                  : 0;
-                    return;
-                }
+            // granules start below 2^31, their last tokens need not
+            const uint32_t at = static_cast<uint32_t>(g) * C::GR + w * C::TS;
+            if (g < seg.g1 && at < static_cast<uint32_t>(seg.kmax)) {
+                ++g;
+                base[i] = static_cast<int>(at);
+                kmax[i] = seg.kmax;
+                hkv[i] = h;
+                const int j = static_cast<int>(at) + (lane % C::MB) * 16;
+                page[i] = j < seg.kmax ? table[j >> p.pool.page_shift] : 0;
+                return;
             }
-            more = walk.next(p, seg);
-            g = seg.g0;
+            segment(p);
         }
     }
+    // offset in a slot of the lane's i-th chunk of a block of 16 rows
+    __device__ static uint32_t place(int lane, int i)
+    {
+        constexpr int CH = C::RB / 16;  // chunks per row
+        if constexpr ((CH & (CH - 1)) == 0 && CH <= 32) {
+            constexpr int STEP = 32 / CH;  // rows per 32 chunks
+            const int r = lane / CH, c = lane % CH;
+            return ((r * C::RBS + ((c ^ C::key(r)) << 4)) ^ (C::key(i * STEP) << 4)) + i * STEP * C::RBS;
+        } else {
+            const int x = lane + 32 * i, r = x / CH, c = x - r * CH;
+            return r * C::RBS + ((c ^ C::key(r)) << 4);
+        }
+    }
+    template <bool VALUE>
     __device__ void issue(const PagedFwdParams& p)
     {
         const int lane = threadIdx.x & 31;
-        const bool value = e & 1u;
         if (base[0] >= 0) {
-            const uint32_t n = e % C::NST;
-            const uint32_t dst = ring + n * C::SLOT;
-            const bool good = page[0] >= 0 && page[0] < p.pool.num_pages;
-            const uint32_t bits = __ballot_sync(0xffffffffu, good);
-            if (lane == 0) {
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(ok + 4u * n), "r"(bits) : "memory");
+            constexpr int CH = C::RB / 16;
+            if constexpr (!VALUE) {
+                const bool good = static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(p.pool.num_pages);
+                bits = __ballot_sync(0xffffffffu, good) & ((1u << C::MB) - 1u);
+                if (!good) record_bad_page(PAGED_FWD);
+                // blocks are at least 1280 bytes, so a pool has fewer than 2^32 of them
+                const uint32_t blk = good ? static_cast<uint32_t>(page[0]) * p.pool.Hkv + hkv[0] : 0u;
+#pragma unroll
+                for (int mb = 0; mb < C::MB; ++mb)
+                    off[mb] = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, blk, mb)) * p.block_bytes +
+                              ((base[0] + mb * 16) & (p.pool.page_size - 1)) * C::RB;
+                if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(ok + 4u * n), "r"(bits) : "memory");
             }
-            if (!value && !good) record_bad_page(PAGED_FWD);
+            const uint8_t* const pool = static_cast<const uint8_t*>(VALUE ? p.v_cache : p.k_cache);
+            const bool whole = kmax[0] - base[0] >= C::TS && bits == (1u << C::MB) - 1u;
 #pragma unroll
             for (int mb = 0; mb < C::MB; ++mb) {
-                const int pg = __shfl_sync(0xffffffffu, page[0], mb);
-                const bool fine = bits >> mb & 1u;
-                const int valid = fine ? min(16, kmax[0] - base[0] - mb * 16) : 0;  // tokens to read (may be <= 0)
+                // 16 rows lie together, and their pairs
+                const uint8_t* const rows = pool + off[mb] + lane * 16;
                 const int slot0 = (base[0] + mb * 16) & (p.pool.page_size - 1);
-                const uint8_t* blk = static_cast<const uint8_t*>(value ? p.v_cache : p.k_cache) +
-                                     (fine ? pool_block<D, INT4>(p.pool, pg, h[0]) : 0);
-                const uint8_t* rows = blk + static_cast<size_t>(slot0) * C::RB;
-                constexpr int CH = C::RB / 16;  // chunks per row
+                const uint8_t* const pairs = rows + (p.pool.page_size * C::RB - slot0 * (C::RB - C::SCB));
+                const uint32_t dst = slot + mb * 16 * C::RBS;
+                const uint32_t pdst = slot + C::TS * C::RBS + mb * 16 * C::SCB + lane * 16;
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const int x = lane + 32 * i, r = x / CH, c = x - r * CH, rr = mb * 16 + r;
-                    const int sw = C::RBS == 64 ? c ^ ((rr >> 1) & 3) : c ^ (rr & 7);
-                    copy16(dst + rr * C::RBS + sw * 16, rows + (r < valid ? r * C::RB + c * 16 : 0), r < valid ? 16u : 0u);
-                }
-                if constexpr (INT4) {
-                    const uint8_t* sc = blk + static_cast<size_t>(p.pool.page_size) * C::RB + static_cast<size_t>(slot0) * C::SCB;
+                    for (int i = 0; i < CH / 2; ++i) copy16(dst + place(lane, i), rows + i * 512);
+                    if constexpr (INT4) {
 #pragma unroll
-                    for (int i = 0; i < (C::SCB + 31) / 32; ++i) {  // SCB chunks of 16 bytes per 16 tokens
-                        const int x = lane + 32 * i;
-                        if (x < C::SCB) {
-                            const int n = max(0, min(16, valid * C::SCB - x * 16));
-                            copy16(dst + C::TS * C::RBS + mb * 16 * C::SCB + x * 16, sc + (n > 0 ? x * 16 : 0), n);
+                        for (int i = 0; i < (C::SCB + 31) / 32; ++i)
+                            if (lane + 32 * i < C::SCB) copy16(pdst + i * 512, pairs + i * 512);
+                    }
+                } else {
+                    // only what exists is read; the rest of the slot is zeros
+                    const int valid = (bits >> mb & 1u) ? max(0, min(16, kmax[0] - base[0] - mb * 16)) : 0;
+#pragma unroll
+                    for (int i = 0; i < CH / 2; ++i) {
+                        const int left = max(0, min(16, valid * C::RB - (lane + 32 * i) * 16));
+                        copy16_part(dst + place(lane, i), left > 0 ? rows + i * 512 : pool, left);
+                    }
+                    if constexpr (INT4) {
+#pragma unroll
+                        for (int i = 0; i < (C::SCB + 31) / 32; ++i) {
+                            const int left = max(0, min(16, valid * C::SCB - (lane + 32 * i) * 16));
+                            if (lane + 32 * i < C::SCB) copy16_part(pdst + i * 512, left > 0 ? pairs + i * 512 : pool, left);
                         }
                     }
                 }
             }
-            if (value) {
+            if constexpr (VALUE) {
                 base[0] = base[1];
                 kmax[0] = kmax[1];
-                h[0] = h[1];
+                hkv[0] = hkv[1];
                 page[0] = page[1];
                 fetch(p, 1);
             }
         }
         copy_commit();
-        ++e;
+        slot += C::SLOT;
+        if (++n == C::NST) {
+            n = 0;
+            slot -= C::NST * C::SLOT;
+        }
     }
 };
 
@@ -527,8 +587,19 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
     PagedLoad<D, INT4, NT> load;
     load.init(p, start, ring, okw);
 #pragma unroll
-    for (int i = 0; i < C::NST - 1; ++i) load.issue(p);
-    uint32_t e = 0;  // copies consumed
+    for (int i = 0; i < C::NST - 1; ++i) {
+        if (i & 1) load.template issue<true>(p);
+        else load.template issue<false>(p);
+    }
+    constexpr bool AHEAD = (C::NST - 1) & 1;  // NST - 1 copies ahead of a key tile: a value tile
+    uint32_t n = 0, at = w * C::NST * C::SLOT;  // the slot consumed next, and its offset
+    auto turn = [&] {
+        at += C::SLOT;
+        if (++n == C::NST) {
+            n = 0;
+            at -= C::NST * C::SLOT;
+        }
+    };
 
     // the mma row of a score tile that holds token (row & 7): at the narrowest rows the
     // tokens are dealt so that the value loads of a warp meet no bank twice
@@ -536,6 +607,13 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         return C::RBS == 64 && INT4 ? (slot & ~3) | ((slot & 1) << 1) | ((slot >> 1) & 1) : slot;
     };
     const int row_a = tok_of(gg);
+    // offsets in a slot of the lane's key words (rows row_a, row_a + 8) and value words
+    // (rows v_row, the next slot's token, and both + 8)
+    const uint32_t key_a = row_a * C::RBS + (C::key(row_a) << 4) + t * 4;
+    const int v_row = tok_of(2 * t);
+    constexpr int V_NEXT = C::RBS == 64 ? 2 : 1;  // tok_of(2 t + 1) - tok_of(2 t); changes key() by 1
+    const uint32_t val_a = v_row * C::RBS + (((gg >> 2) ^ C::key(v_row)) << 4) + (gg & 3) * 4;
+    const uint32_t pair_a = v_row * C::SCB + (gg >> 2) * 4;
 
     PagedWalk<C> walk;
     walk.init(p, start);
@@ -566,16 +644,17 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         const int lim0 = p.causal ? min(x.s.Sk, x.r0 / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;  // the least
 
         for (int g = x.g0; g < x.g1; ++g) {
-            if (static_cast<long long>(g) * C::GR + w * C::TS >= x.kmax) break;
-            const int base = g * C::GR + w * C::TS;
+            const uint32_t at0 = static_cast<uint32_t>(g) * C::GR + w * C::TS;
+            if (at0 >= static_cast<uint32_t>(x.kmax)) break;
+            const int base = static_cast<int>(at0);
             // ---- scores
             copy_wait<C::NST - 2>();
             __syncwarp();
-            load.issue(p);  // into the slot consumed last
-            const uint32_t at = (w * C::NST + e % C::NST) * C::SLOT;  // offset of the slot
-            const uint8_t* const ks = smem + at;
-            const uint32_t bits = lds<uint32_t>(smem + C::OFF_OK + (w * C::NST + e % C::NST) * 4);
-            ++e;
+            load.template issue<AHEAD>(p);  // into the slot consumed last
+            const uint32_t kat = at;
+            const uint8_t* const ks = smem + kat;
+            const uint32_t bits = lds<uint32_t>(smem + C::OFF_OK + (w * C::NST + n) * 4);
+            turn();
             float s[MB][NT][4];
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
@@ -585,7 +664,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     for (int i = 0; i < 4; ++i) s[mb][nt][i] = 0.0f;
             if constexpr (!INT4) {
                 const int r = lane & 15;
-                const uint32_t row = sbase + at + r * C::RBS;
+                const uint32_t row = sbase + kat + r * C::RBS;
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
                     uint32_t a0[4], a1[4];
@@ -608,7 +687,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint8_t* a = ks + C::TS * C::RBS + (mb * 16 + y * 8 + row_a) * C::SCB + k4 * 4;
+                            const uint8_t* a = ks + row_a * C::SCB + (C::TS * C::RBS + (mb * 16 + y * 8) * C::SCB + k4 * 4);
                             if constexpr (KG == 4) {
                                 const uint4 v = lds<uint4>(a);
                                 pr[mb][y][0] = v.x;
@@ -633,18 +712,17 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                         }
 #pragma unroll
                         for (int mb = 0; mb < MB; ++mb) {
-                            const int ra = mb * 16 + row_a, rb = ra + 8;
-                            const int ca = C::RBS == 64 ? k ^ ((ra >> 1) & 3) : k ^ (ra & 7);
-                            const int cb = C::RBS == 64 ? k ^ ((rb >> 1) & 3) : k ^ (rb & 7);
-                            const uint32_t wa = lds<uint32_t>(ks + ra * C::RBS + ca * 16 + t * 4);
-                            const uint32_t wb = lds<uint32_t>(ks + rb * C::RBS + cb * 16 + t * 4);
-                            const uint32_t a0[4] = {code_tiny<0>(wa), code_tiny<0>(wb), code_tiny<1>(wa), code_tiny<1>(wb)};
-                            const uint32_t a1[4] = {code_tiny<2>(wa), code_tiny<2>(wb), code_tiny<3>(wa), code_tiny<3>(wb)};
+                            const uint8_t* const wk = ks + (key_a ^ ((k & C::LINE) << 4)) +
+                                                      (((k * 16) & ~(C::LINE * 16 + 15)) + mb * 16 * C::RBS);
+                            const uint32_t wa = lds<uint32_t>(wk), wb = lds<uint32_t>(wk + 8 * C::RBS);
+                            const uint32_t a0[4] = {code_tiny<false>(wa), code_tiny<false>(wb), code_tiny<true>(wa), code_tiny<true>(wb)};
+                            const uint32_t a1[4] = {code_tiny<false>(wa >> 8), code_tiny<false>(wb >> 8), code_tiny<true>(wa >> 8),
+                                                    code_tiny<true>(wb >> 8)};
                             const float2 za = pg_unpack2<BF16>(pr[mb][0][kk]), zb = pg_unpack2<BF16>(pr[mb][1][kk]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma16816<BF16>(d, a0, b[nt].x, b[nt].y);
+                                float d[4];
+                                mma16816_first<BF16>(d, a0, b[nt].x, b[nt].y);
                                 mma16816<BF16>(d, a1, b[nt].z, b[nt].w);
                                 s[mb][nt][0] = fmaf(za.x, d[0], fmaf(za.y, qs[nt].x, s[mb][nt][0]));
                                 s[mb][nt][1] = fmaf(za.x, d[1], fmaf(za.y, qs[nt].y, s[mb][nt][1]));
@@ -728,10 +806,10 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             // ---- O^T += V^T P^T
             copy_wait<C::NST - 2>();
             __syncwarp();
-            load.issue(p);
-            const uint32_t vat = (w * C::NST + e % C::NST) * C::SLOT;
+            load.template issue<!AHEAD>(p);
+            const uint32_t vat = at;
             const uint8_t* const vs = smem + vat;
-            ++e;
+            turn();
             if constexpr (!INT4) {
                 const int r = (lane & 7) + ((lane >> 4) << 3);
                 const uint32_t row = sbase + vat + r * C::RBS;
@@ -748,38 +826,47 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             } else {
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
-                    const int tk[4] = {mb * 16 + tok_of(2 * t), mb * 16 + tok_of(2 * t + 1), mb * 16 + tok_of(2 * t + 8),
-                                       mb * 16 + tok_of(2 * t + 9)};
 #pragma unroll
                     for (int ws = 0; ws < D / 64; ++ws) {  // 64 dims: word gg of eight
                         uint32_t wd[4], pr[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int c = 2 * ws + (gg >> 2);
-                            const int sw = C::RBS == 64 ? c ^ ((tk[i] >> 1) & 3) : c ^ (tk[i] & 7);
-                            wd[i] = lds<uint32_t>(vs + tk[i] * C::RBS + sw * 16 + (gg & 3) * 4);
-                            pr[i] = lds<uint32_t>(vs + C::TS * C::RBS + tk[i] * C::SCB + c * 4);
+                            const int row = mb * 16 + (i & 1) * V_NEXT + (i >> 1) * 8;
+                            wd[i] = lds<uint32_t>(vs + (val_a ^ ((((2 * ws) & C::LINE) ^ (i & 1)) << 4)) +
+                                                  (row * C::RBS + ((2 * ws * 16) & ~(C::LINE * 16 + 15))));
+                            pr[i] = lds<uint32_t>(vs + pair_a + (C::TS * C::RBS + row * C::SCB + ws * 8));
                         }
                         const uint32_t lo01 = __byte_perm(wd[0], wd[1], 0x5410), hi01 = __byte_perm(wd[0], wd[1], 0x7632);
                         const uint32_t lo23 = __byte_perm(wd[2], wd[3], 0x5410), hi23 = __byte_perm(wd[2], wd[3], 0x7632);
                         const uint32_t s01 = __byte_perm(pr[0], pr[1], 0x5410), z01 = __byte_perm(pr[0], pr[1], 0x7632);
                         const uint32_t s23 = __byte_perm(pr[2], pr[3], 0x5410), z23 = __byte_perm(pr[2], pr[3], 0x7632);
-                        auto tile = [&](auto P) {
-                            constexpr int j = decltype(P)::value;
-                            const uint32_t a[4] = {fma16x2<BF16>(code_value<BF16, j>(lo01), s01, z01),
-                                                   fma16x2<BF16>(code_value<BF16, j>(hi01), s01, z01),
-                                                   fma16x2<BF16>(code_value<BF16, j>(lo23), s23, z23),
-                                                   fma16x2<BF16>(code_value<BF16, j>(hi23), s23, z23)};
+                        uint32_t s01q = s01, s23q = s23;
+                        if constexpr (BF16) {
+                            s01q = mul_bf16x2(s01, 0x40804080u);
+                            s23q = mul_bf16x2(s23, 0x40804080u);
+                        }
+                        // tile j of the 64 dims: rows gg and gg + 8 are dims j and 4 + j of the word
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int sh = (j >> 1) * 8;
+                            uint32_t a[4];
+                            if (j & 1) {
+                                a[0] = code_value<BF16, true>(lo01 >> sh, s01, s01q, z01);
+                                a[1] = code_value<BF16, true>(hi01 >> sh, s01, s01q, z01);
+                                a[2] = code_value<BF16, true>(lo23 >> sh, s23, s23q, z23);
+                                a[3] = code_value<BF16, true>(hi23 >> sh, s23, s23q, z23);
+                            } else {
+                                a[0] = code_value<BF16, false>(lo01 >> sh, s01, s01q, z01);
+                                a[1] = code_value<BF16, false>(hi01 >> sh, s01, s01q, z01);
+                                a[2] = code_value<BF16, false>(lo23 >> sh, s23, s23q, z23);
+                                a[3] = code_value<BF16, false>(hi23 >> sh, s23, s23q, z23);
+                            }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 mma16816<BF16>(o[ws * 4 + j][nt], a, ph[mb][nt][0], ph[mb][nt][1]);
                                 mma16816<BF16>(o[ws * 4 + j][nt], a, pl[mb][nt][0], pl[mb][nt][1]);
                             }
-                        };
-                        tile(std::integral_constant<int, 0>{});
-                        tile(std::integral_constant<int, 1>{});
-                        tile(std::integral_constant<int, 2>{});
-                        tile(std::integral_constant<int, 3>{});
+                        }
                     }
                 }
             }
