@@ -91,8 +91,8 @@ int paged_tiles(int max_q, int group, int d)
     return nt;
 }
 
-// Resident CTAs of the forward's grid, at most: two per SM.
-int paged_grid_max(int sm_count) { return 2 * sm_count; }
+// Resident CTAs of the forward's grid, at most.
+int paged_grid_max(int sm_count) { return fa::kPagedCtas * sm_count; }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 

@@ -118,50 +118,6 @@ __device__ __forceinline__ T lds(const uint8_t* a)
 {
     return *reinterpret_cast<const T*>(a);
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t fma16x2(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t d;
-    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    if constexpr (BF16) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// Codes in a 32-bit word, in bits 0 .. 3 (HIGH: 4 .. 7) of both halves.
-template <bool HIGH>
-__device__ __forceinline__ uint32_t code_tiny(uint32_t w)
-{
-    return w & (HIGH ? 0x00f000f0u : 0x000f000fu);
-}
-// scale * code + zero of a pair.  s4: 4 scale (bf16).
-template <bool BF16, bool HIGH>
-__device__ __forceinline__ uint32_t code_value(uint32_t w, uint32_t s, uint32_t s4, uint32_t z)
-{
-    if constexpr (BF16 && HIGH)  // 2^-129 code, times 2^127
-        return fma16x2<true>(mul_bf16x2(w & 0x00f000f0u, 0x7f007f00u), s4, z);
-    else if constexpr (BF16)     // 128 + code
-        return fma16x2<true>(add16x2<true>((w & 0x000f000fu) | 0x43004300u, 0xc300c300u), s, z);
-    else if constexpr (HIGH)     // 64 + code
-        return fma16x2<false>(add16x2<false>((w & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s, z);
-    else                         // 1024 + code
-        return fma16x2<false>(add16x2<false>((w & 0x000f000fu) | 0x64006400u, 0xe400e400u), s, z);
-}
-
 // ---------------------------------------------------------------------------------
 // Parameters
 // ---------------------------------------------------------------------------------
@@ -188,11 +144,14 @@ struct PagedFwdParams {
     PagedRecord* rec;  // [grid]
 };
 
+// CTAs per SM, at most; the workspace has pieces for as many.
+constexpr int kPagedCtas = 2;
+
 template <int D, bool INT4, int NT>
 struct PagedCfg {
     static constexpr int TS = INT4 ? 32 : 16;      // tokens of a warp's step
     static constexpr int MB = TS / 16;
-    static constexpr int W = INT4 && D == 128 && NT == 1 ? 8 : 4;  // warps
+    static constexpr int W = INT4 && D == 128 && NT == 1 ? 6 : 4;  // warps
     static constexpr int ROWS = 8 * NT;
     static constexpr int GR = W * TS;              // tokens of a granule
     static constexpr int RB = INT4 ? D / 2 : 2 * D;  // bytes of a row (codes)
@@ -202,6 +161,7 @@ struct PagedCfg {
     // slots of a warp's ring, K and V taking turns; what two CTAs per SM (one at the
     // widest rows) leave in shared memory
     static constexpr int CTAS = D >= (INT4 ? 384 : 256) ? 1 : 2;
+    static_assert(CTAS <= kPagedCtas, "workspace pieces");
     static constexpr int ROOM = (CTAS == 1 ? 200 : 88) * 1024;
     static constexpr int NST_ = ROOM / (W * SLOT);
     static constexpr int NST = NST_ > 6 ? 6 : NST_;
@@ -757,7 +717,8 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float v = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
-                    if constexpr (MB == 2) v = fmaxf(v, fmaxf(s[1][nt][i], s[1][nt][2 + i]));
+#pragma unroll
+                    for (int mb = 1; mb < MB; ++mb) v = fmaxf(v, fmaxf(s[mb][nt][i], s[mb][nt][2 + i]));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
