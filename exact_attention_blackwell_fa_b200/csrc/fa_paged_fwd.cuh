@@ -158,23 +158,27 @@ struct PagedCfg {
     static constexpr int RBS = RB <= 64 ? 64 : (RB + 127) / 128 * 128;  // its pitch
     static constexpr int SCB = INT4 ? D / 8 : 0;   // bytes of a row's (scale, zero) pairs
     static constexpr uint32_t SLOT = TS * (RBS + SCB);
-    // slots of a warp's ring, K and V taking turns; what two CTAs per SM (one at the
-    // widest rows) leave in shared memory
     static constexpr int CTAS = D >= (INT4 ? 384 : 256) ? 1 : 2;
     static_assert(CTAS <= kPagedCtas, "workspace pieces");
-    static constexpr int ROOM = (CTAS == 1 ? 200 : 88) * 1024;
-    static constexpr int NST_ = ROOM / (W * SLOT);
+    // Q of a unit, twice: the next unit's is fetched while the last one's O is joined.
+    // B fragments [NT][D / 32][32 lanes][4], sums over groups [NT][D / 32][8], score
+    // factors [NT][8]
+    static constexpr uint32_t OFF_QS = NT * D * 16;
+    static constexpr uint32_t OFF_F = OFF_QS + (INT4 ? NT * D : 0);
+    static constexpr uint32_t Q_BYTES = OFF_F + NT * 32;
+    static constexpr int DP = D <= 192 ? D : 128;  // dims of O joined at a time
+    static constexpr int MP = DP + 4;              // their pitch, 4 mod 16: conflict-free
+    static constexpr uint32_t OFF_Q = 0;
+    static constexpr uint32_t OFF_ML = 2 * Q_BYTES;                    // [2][W][ROWS] (m, l)
+    static constexpr uint32_t OFF_RED = OFF_ML + 2 * W * ROWS * 8;     // [W][8][MP]
+    static constexpr uint32_t OFF_OK = OFF_RED + W * 8 * MP * 4;       // [W][8] blocks of a slot that have a page
+    static constexpr uint32_t OFF_RING = (OFF_OK + W * 32 + 127u) & ~127u;
+    // the rest are the warps' rings, K and V taking turns in their slots
+    static constexpr uint32_t LIMIT = (CTAS == 1 ? 226 : 112) * 1024;
+    static constexpr int NST_ = (LIMIT - OFF_RING) / (W * SLOT);
     static constexpr int NST = NST_ > 6 ? 6 : NST_;
     static_assert(NST >= 3, "ring depth");
-    static constexpr uint32_t OFF_Q = W * NST * SLOT;            // B fragments of Q: [NT][D / 32][32 lanes][4]
-    static constexpr uint32_t OFF_QS = OFF_Q + NT * D * 16;      // sums of Q over groups: [NT][D / 32][8]
-    static constexpr uint32_t OFF_F = OFF_QS + (INT4 ? NT * D : 0);  // score factors [NT][8]
-    static constexpr uint32_t OFF_ML = OFF_F + NT * 32;          // [W][ROWS] (m, l)
-    static constexpr uint32_t OFF_OK = OFF_ML + W * ROWS * 8;    // [W][NST] blocks of a slot that have a page
-    static constexpr uint32_t OFF_RED = (OFF_OK + W * NST * 4 + 15u) & ~15u;  // [W][8][MP] a part of O
-    static constexpr int MP = 68;                                // 64 dims; pitch 4 mod 16: conflict-free
-    static constexpr uint32_t SMEM = OFF_RED + W * 8 * MP * 4;
-    static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
+    static constexpr uint32_t SMEM = OFF_RING + W * NST * SLOT;
     static constexpr int THREADS = W * 32;
     // 16-byte chunk c of row r lies at chunk c ^ key(r) of its 64- or 128-byte line, so
     // that the fragment loads of a warp meet no bank twice
@@ -456,7 +460,7 @@ struct PagedLoad {
 // Q of a unit into shared memory, as the B fragments of the score products.
 // ---------------------------------------------------------------------------------
 template <int D, bool BF16, bool INT4, int NT>
-__device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const PagedSegment& x, uint8_t* smem)
+__device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const PagedSegment& x, uint8_t* to)
 {
     using C = PagedCfg<D, INT4, NT>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
@@ -467,7 +471,7 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
         const bool ok = r < x.R;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) +
                               (static_cast<size_t>(x.s.q0 + (ok ? tok : 0)) * p.Hq + h0 + (ok ? r - tok * p.group : 0)) * D;
-        uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_Q) + nt * (D / 32) * 32 + lane;
+        uint4* dst = reinterpret_cast<uint4*>(to) + nt * (D / 32) * 32 + lane;
         if constexpr (!INT4) {
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {  // two steps of 16 dims
@@ -505,7 +509,7 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
                 for (int i = 0; i < 8; ++i) sum += f[i];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (t == 0) reinterpret_cast<float*>(smem + C::OFF_QS)[(nt * (D / 32) + k) * 8 + gg] = sum * down;
+                if (t == 0) reinterpret_cast<float*>(to + C::OFF_QS)[(nt * (D / 32) + k) * 8 + gg] = sum * down;
                 uint32_t b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -516,7 +520,7 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
             }
             // the score's factor undoes both
             if (t == 0)
-                reinterpret_cast<float*>(smem + C::OFF_F)[nt * 8 + gg] = p.sl2 * __uint_as_float(static_cast<uint32_t>(dn + 127) << 23);
+                reinterpret_cast<float*>(to + C::OFF_F)[nt * 8 + gg] = p.sl2 * __uint_as_float(static_cast<uint32_t>(dn + 127) << 23);
         }
     }
 }
@@ -542,8 +546,8 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
     if (threadIdx.x == 0) p.rec[blockIdx.x].last = -1;
     if (start.lo >= start.hi) return;
 
-    const uint32_t ring = sbase + w * C::NST * C::SLOT;
-    const uint32_t okw = sbase + C::OFF_OK + w * C::NST * 4;
+    const uint32_t ring = sbase + C::OFF_RING + w * C::NST * C::SLOT;
+    const uint32_t okw = sbase + C::OFF_OK + w * 32;
     PagedLoad<D, INT4, NT> load;
     load.init(p, start, ring, okw);
 #pragma unroll
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         else load.template issue<false>(p);
     }
     constexpr bool AHEAD = (C::NST - 1) & 1;  // NST - 1 copies ahead of a key tile: a value tile
-    uint32_t n = 0, at = w * C::NST * C::SLOT;  // the slot consumed next, and its offset
+    uint32_t n = 0, at = C::OFF_RING + w * C::NST * C::SLOT;  // the slot consumed next, and its offset
     auto turn = [&] {
         at += C::SLOT;
         if (++n == C::NST) {
@@ -577,12 +581,13 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 
     PagedWalk<C> walk;
     walk.init(p, start);
-    PagedSegment x;
-    while (walk.next(p, x)) {
-        __syncthreads();  // the last unit's Q and partial sums are done with
-        paged_stage_q<D, BF16, INT4, NT>(p, x, smem);
-        __syncthreads();
-
+    PagedSegment x, following;
+    bool more = walk.next(p, x);  // the range is not empty
+    uint32_t turns = 0;           // which of the two places for Q and for (m, l)
+    paged_stage_q<D, BF16, INT4, NT>(p, x, smem + C::OFF_Q);
+    __syncthreads();
+    for (; more; x = following, turns ^= 1u) {
+        const uint8_t* const sq = smem + C::OFF_Q + turns * C::Q_BYTES;
         float o[MT][NT][4];
         float m[NT][2], l[NT][2], f[NT][2];
         int lim[NT][2];
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                 m[nt][i] = -INFINITY;
                 l[nt][i] = 0.0f;
                 const int r = x.r0 + nt * 8 + 2 * t + i;
-                f[nt][i] = INT4 ? reinterpret_cast<const float*>(smem + C::OFF_F)[nt * 8 + 2 * t + i] : p.sl2;
+                f[nt][i] = INT4 ? reinterpret_cast<const float*>(sq + C::OFF_F)[nt * 8 + 2 * t + i] : p.sl2;
                 lim[nt][i] = p.causal && r < x.R ? min(x.s.Sk, r / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;
             }
         }
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             load.template issue<AHEAD>(p);  // into the slot consumed last
             const uint32_t kat = at;
             const uint8_t* const ks = smem + kat;
-            const uint32_t bits = lds<uint32_t>(smem + C::OFF_OK + (w * C::NST + n) * 4);
+            const uint32_t bits = lds<uint32_t>(smem + C::OFF_OK + (w * 8 + n) * 4);
             turn();
             float s[MB][NT][4];
 #pragma unroll
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     ldmatrix4(a1, row + (((c + 2) ^ (r & 7)) << 4));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 b = lds<uint4>(smem + C::OFF_Q + ((nt * (D / 32) + k) * 32 + lane) * 16);
+                        const uint4 b = lds<uint4>(sq + ((nt * (D / 32) + k) * 32 + lane) * 16);
                         mma16816<BF16>(s[0][nt], a0, b.x, b.y);
                         mma16816<BF16>(s[0][nt], a1, b.z, b.w);
                     }
@@ -667,8 +672,8 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                         float2 qs[NT];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            b[nt] = lds<uint4>(smem + C::OFF_Q + ((nt * (D / 32) + k) * 32 + lane) * 16);
-                            qs[nt] = lds<float2>(smem + C::OFF_QS + ((nt * (D / 32) + k) * 8 + 2 * t) * 4);
+                            b[nt] = lds<uint4>(sq + ((nt * (D / 32) + k) * 32 + lane) * 16);
+                            qs[nt] = lds<float2>(sq + C::OFF_QS + ((nt * (D / 32) + k) * 8 + 2 * t) * 4);
                         }
 #pragma unroll
                         for (int mb = 0; mb < MB; ++mb) {
@@ -843,10 +848,12 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 if (gg == 0)
-                    reinterpret_cast<float2*>(smem + C::OFF_ML)[w * C::ROWS + nt * 8 + 2 * t + i] = make_float2(m[nt][i], v);
+                    reinterpret_cast<float2*>(smem + C::OFF_ML)[(turns * C::W + w) * C::ROWS + nt * 8 + 2 * t + i] = make_float2(m[nt][i], v);
             }
+        more = walk.next(p, following);
+        if (more) paged_stage_q<D, BF16, INT4, NT>(p, following, smem + C::OFF_Q + (turns ^ 1u) * C::Q_BYTES);
         __syncthreads();
-        const float2* ml = reinterpret_cast<const float2*>(smem + C::OFF_ML);
+        const float2* const ml = reinterpret_cast<const float2*>(smem + C::OFF_ML) + turns * C::W * C::ROWS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -868,17 +875,17 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int part = 0; part < D / 64; ++part) {
+            for (int part = 0; part < D / C::DP; ++part) {
                 if (nt + part > 0) __syncthreads();
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
+                for (int y = 0; y < C::DP / 16; ++y)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        buf[(w * 8 + 2 * t + (i & 1)) * C::MP + y * 16 + (i >> 1) * 8 + gg] = o[part * 4 + y][nt][i];
+                        buf[(w * 8 + 2 * t + (i & 1)) * C::MP + y * 16 + (i >> 1) * 8 + gg] = o[part * (C::DP / 16) + y][nt][i];
                 __syncthreads();
                 // thread: row rr of the tile, eight neighbouring dims (word v of the part)
-                for (int y = threadIdx.x; y < 64; y += C::THREADS) {
-                    const int rr = y >> 3, v = y & 7, r = x.r0 + nt * 8 + rr;
+                for (int y = threadIdx.x; y < C::DP; y += C::THREADS) {
+                    const int rr = y / (C::DP / 8), v = y - rr * (C::DP / 8), r = x.r0 + nt * 8 + rr;
                     if (r >= x.R) continue;
                     float acc[8];
 #pragma unroll
@@ -888,7 +895,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             // place of dim 8 v + i of the part in the tiles
-                            const int at = INT4 ? (i & 3) * 16 + (i >> 2) * 8 + v : 8 * v + i;
+                            const int at = INT4 ? (v >> 3) * 64 + (i & 3) * 16 + (i >> 2) * 8 + (v & 7) : 8 * v + i;
                             acc[i] += buf[(ww * 8 + rr) * C::MP + at];
                         }
                     float top = -INFINITY, sum = 0.0f;
@@ -905,13 +912,13 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
                         for (int i = 0; i < 8; ++i) acc[i] *= inv;
                         reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
-                                                 (static_cast<size_t>(x.s.q0 + tok) * p.Hq + h) * D + part * 64)[v] =
+                                                 (static_cast<size_t>(x.s.q0 + tok) * p.Hq + h) * D + part * C::DP)[v] =
                             pg_pack8<BF16>(acc);
                         if (part == 0 && v == 0)
                             p.lse[static_cast<size_t>(h) * p.total_q + x.s.q0 + tok] =
                                 sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(p.opart + (piece + nt * 8 + rr) * D + part * 64 + v * 8);
+                        float4* dst = reinterpret_cast<float4*>(p.opart + (piece + nt * 8 + rr) * D + part * C::DP + v * 8);
                         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
                         dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
                         if (part == 0 && v == 0) p.mlpart[piece + nt * 8 + rr] = make_float2(top, sum);
