@@ -72,12 +72,13 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype_code(t) -> int:
+    dtype = t if isinstance(t, torch.dtype) else t.dtype
+    if dtype == torch.bfloat16:
         return _lib.FA_BF16
-    if t.dtype == torch.float16:
+    if dtype == torch.float16:
         return _lib.FA_FP16
-    raise TypeError(f"fa: inputs must be bf16 or fp16, got {t.dtype}")
+    raise TypeError(f"fa: inputs must be bf16 or fp16, got {dtype}")
 
 
 def _check(t: torch.Tensor, name: str, dtype=None):
@@ -347,7 +348,14 @@ class _Here:
 _HERE = _Here()
 
 
-def _on(device):
+def _on(device, stream=None):
+    """Makes `device` current, and `stream` if one is given: what a call allocates then
+    belongs to the stream that it runs on, so its memory is not handed out again while
+    that stream still uses it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        return torch.cuda.stream(stream)
     return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
@@ -419,19 +427,20 @@ def fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, 
             raise ValueError("fa: q must be [total, Hq, d]")
         Hq = q.shape[1]
         q_stride = _token_rows(q, "q", total, Hq, d, dtype, device)
-        if q_out is None:
-            q_out = torch.empty((total, Hq, d), dtype=dtype, device=device)
-        else:
+        if q_out is not None:
             _check(q_out, "q_out", dtype)
             _shape(q_out, "q_out", (total, Hq, d))
+            _same_device(k, q_out=q_out)
     elif q_out is not None:
         raise ValueError("fa: q_out without q")
     rot = 0
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", torch.float32)
         rot = 2 * inv_freq.numel()
-    _same_device(k, q_out=q_out, inv_freq=inv_freq)
-    with _on(device):
+        _same_device(k, inv_freq=inv_freq)
+    with _on(device, stream):
+        if q is not None and q_out is None:
+            q_out = q.new_empty((total, Hq, d))
         code = _lib.load().fa_kv_append(
             q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
             q_out.data_ptr() if q is not None else None, k_cache.data_ptr(), v_cache.data_ptr(),
@@ -457,14 +466,15 @@ def fa_kv_gather(k_cache, v_cache, cu_seqlens_k, block_table, total_k: int, dtyp
     _check_index(cu_seqlens_k, "cu_seqlens_k", (B + 1,), device)
     total_k = int(total_k)
     shape = (total_k, Hkv, d)
-    k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=device) if v is None else v
-    dt = _dtype_code(k)
+    dt = _dtype_code(dtype)
     for name, t in (("k", k), ("v", v)):
-        _check(t, name, dtype)
-        _shape(t, name, shape)
-    _same_device(k_cache, k=k, v=v)
-    with _on(device):
+        if t is not None:
+            _check(t, name, dtype)
+            _shape(t, name, shape)
+            _same_device(k_cache, **{name: t})
+    with _on(device, stream):
+        k = k_cache.new_empty(shape, dtype=dtype) if k is None else k
+        v = k_cache.new_empty(shape, dtype=dtype) if v is None else v
         code = _lib.load().fa_kv_gather(k_cache.data_ptr(), v_cache.data_ptr(), k.data_ptr(), v.data_ptr(),
                                         cu_seqlens_k.data_ptr(), block_table.data_ptr(), B, total_k, Hkv, d,
                                         page_size, num_pages, max_pages, fmt, dt, _stream_ptr(stream))
@@ -495,20 +505,20 @@ def fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_
         raise ValueError(f"fa: the pools hold head_dim {dk}, q has {d}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check(out, "out", dtype)
-        _shape(out, "out", q.shape)
-    if lse is None:
-        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=device)
-    else:
-        _check(lse, "lse", torch.float32)
-        _shape(lse, "lse", (Hq, total_q))
-    _same_device(q, out=out, lse=lse)
+    for name, t, kind, shape in (("out", out, dtype, q.shape), ("lse", lse, torch.float32, (Hq, total_q))):
+        if t is not None:
+            _check(t, name, kind)
+            _shape(t, name, shape)
+            _same_device(q, **{name: t})
     lib = _lib.load()
-    with _on(device):
-        workspace = _workspace(workspace, q, lib.fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d))
+    with _on(device, stream):
+        out = torch.empty_like(q) if out is None else out
+        lse = q.new_empty((Hq, total_q), dtype=torch.float32) if lse is None else lse
+        need = lib.fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d)
+        if workspace is None:
+            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+        else:
+            _workspace(workspace, q, need)
         code = lib.fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                 lse.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
                                 block_table.data_ptr(), B, max_seqlen_q, total_q, Hq, Hkv, d, page_size,

@@ -151,7 +151,7 @@ template <int D, bool INT4, int NT>
 struct PagedCfg {
     static constexpr int TS = INT4 ? 32 : 16;      // tokens of a warp's step
     static constexpr int MB = TS / 16;
-    static constexpr int W = INT4 && D == 128 && NT == 1 ? 6 : 4;  // warps
+    static constexpr int W = D == 128 && NT == 1 ? 6 : 4;  // warps
     static constexpr int ROWS = 8 * NT;
     static constexpr int GR = W * TS;              // tokens of a granule
     static constexpr int RB = INT4 ? D / 2 : 2 * D;  // bytes of a row (codes)
@@ -176,7 +176,10 @@ struct PagedCfg {
     // the rest are the warps' rings, K and V taking turns in their slots
     static constexpr uint32_t LIMIT = (CTAS == 1 ? 226 : 112) * 1024;
     static constexpr int NST_ = (LIMIT - OFF_RING) / (W * SLOT);
-    static constexpr int NST = NST_ > 6 ? 6 : NST_;
+    // deeper rings of 16-bit rows are slower (d = 256, 4 sequences of 131,072 tokens: 168 us
+    // with four slots, 183 with six): 64 to 128 KB in flight per SM cover the latency
+    static constexpr int MOST = INT4 ? 6 : 4;
+    static constexpr int NST = NST_ > MOST ? MOST : NST_;
     static_assert(NST >= 3, "ring depth");
     static constexpr uint32_t SMEM = OFF_RING + W * NST * SLOT;
     static constexpr int THREADS = W * 32;
@@ -225,22 +228,23 @@ template <class C>
 __device__ __forceinline__ void paged_start(const PagedFwdParams& p, PagedStart* out, long long* red)
 {
     const int T = blockDim.x, tid = threadIdx.x;
-    long long mine = 0;
-    for (int b = tid; b < p.B; b += T) {
+    auto granules = [&](int b) {
+        if (b >= p.B) return 0ll;
         const PagedSeq s = paged_seq<C>(p, b);
-        mine += static_cast<long long>(s.nu) * s.kt;
-        if (blockIdx.x == 0 && p.seqlens_k[b] > (p.pool.max_pages << p.pool.page_shift)) record_bad_page(PAGED_FWD);
-    }
+        return static_cast<long long>(s.nu) * s.kt;
+    };
+    long long mine = granules(tid);
+    const long long first = mine;
+    for (int b = tid + T; b < p.B; b += T) mine += granules(b);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += T)
+            if (p.seqlens_k[b] > (p.pool.max_pages << p.pool.page_shift)) record_bad_page(PAGED_FWD);
     const long long total = block_sum(mine, red);
     const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
     if (tid == 0) *out = PagedStart{0, 0, lo, hi, total};
     long long before = 0;
-    for (int c = 0; c < p.B; c += T) {  // T sequences at a time: an inclusive sum over the block
-        long long x = 0;
-        if (c + tid < p.B) {
-            const PagedSeq s = paged_seq<C>(p, c + tid);
-            x = static_cast<long long>(s.nu) * s.kt;
-        }
+    for (int c = 0; c < p.B && before <= lo; c += T) {  // T sequences at a time: an inclusive sum over the block
+        long long x = c == 0 ? first : granules(c + tid);
         const long long own = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -465,63 +469,66 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
     using C = PagedCfg<D, INT4, NT>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
     const int h0 = (x.u % p.pool.Hkv) * p.group;
-    for (int nt = w; nt < NT; nt += C::W) {
-        const int r = x.r0 + nt * 8 + gg;
-        const int tok = r / p.group;
-        const bool ok = r < x.R;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                              (static_cast<size_t>(x.s.q0 + (ok ? tok : 0)) * p.Hq + h0 + (ok ? r - tok * p.group : 0)) * D;
-        uint4* dst = reinterpret_cast<uint4*>(to) + nt * (D / 32) * 32 + lane;
-        if constexpr (!INT4) {
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {  // two steps of 16 dims
-                const uint32_t* s = reinterpret_cast<const uint32_t*>(src + k * 32) + t;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (ok) v = make_uint4(s[0], s[4], s[8], s[12]);
-                dst[k * 32] = v;
-            }
-        } else {
-            // dims 8 t .. 8 t + 7 of each group: pairs (i, i + 4)
-            uint4 v[D / 32];
-            float big = 0.0f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                v[k] = ok ? reinterpret_cast<const uint4*>(src + k * 32)[t] : make_uint4(0u, 0u, 0u, 0u);
-                float f[8];
-                pg_unpack8<BF16>(v[k], f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[i]));
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // the row's power of two: its largest value comes to 2^62 (bf16) or 2^14 (fp16)
-            const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-            const int kq = BF16 ? max(7, min(100, 62 - ex)) : max(-2, min(38, 14 - ex));
-            const float up = __uint_as_float(static_cast<uint32_t>(kq + 127) << 23);
-            // the codes are 2^-133 (bf16) or 2^-24 (fp16) small
-            const int dn = (BF16 ? 133 : 24) - kq;  // 33 .. 126 or -14 .. 26
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - dn) << 23);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                float f[8], sum = 0.0f;
-                pg_unpack8<BF16>(v[k], f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum += f[i];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (t == 0) reinterpret_cast<float*>(to + C::OFF_QS)[(nt * (D / 32) + k) * 8 + gg] = sum * down;
-                uint32_t b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = (i & 1) ? up * 0.0625f : up;
-                    b[i] = pg_pack2<BF16>(f[i] * u, f[i + 4] * u);
-                }
-                dst[k * 32] = make_uint4(b[0], b[1], b[2], b[3]);
-            }
-            // the score's factor undoes both
-            if (t == 0)
-                reinterpret_cast<float*>(to + C::OFF_F)[nt * 8 + gg] = p.sl2 * __uint_as_float(static_cast<uint32_t>(dn + 127) << 23);
+    // the warps of a tile share its blocks of 32 dims
+    static_assert(C::W % NT == 0, "warps per tile");
+    constexpr int PER = C::W / NT;
+    const int nt = w % NT, k0 = w / NT;
+    const int r = x.r0 + nt * 8 + gg;
+    const int tok = r / p.group;
+    const bool ok = r < x.R;
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                          (static_cast<size_t>(x.s.q0 + (ok ? tok : 0)) * p.Hq + h0 + (ok ? r - tok * p.group : 0)) * D;
+    uint4* dst = reinterpret_cast<uint4*>(to) + nt * (D / 32) * 32 + lane;
+    if constexpr (!INT4) {
+#pragma unroll 4
+        for (int k = k0; k < D / 32; k += PER) {  // two steps of 16 dims
+            const uint32_t* s = reinterpret_cast<const uint32_t*>(src + k * 32) + t;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (ok) v = make_uint4(s[0], s[4], s[8], s[12]);
+            dst[k * 32] = v;
         }
+    } else {
+        // dims 8 t .. 8 t + 7 of each group: pairs (i, i + 4).  Read twice: O is live here
+        auto dims = [&](int k, float (&f)[8]) {
+            pg_unpack8<BF16>(ok ? reinterpret_cast<const uint4*>(src + k * 32)[t] : make_uint4(0u, 0u, 0u, 0u), f);
+        };
+        float big = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < D / 32; ++k) {
+            float f[8];
+            dims(k, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[i]));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // the row's power of two: its largest value comes to 2^62 (bf16) or 2^14 (fp16)
+        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+        const int kq = BF16 ? max(7, min(100, 62 - ex)) : max(-2, min(38, 14 - ex));
+        const float up = __uint_as_float(static_cast<uint32_t>(kq + 127) << 23);
+        // the codes are 2^-133 (bf16) or 2^-24 (fp16) small
+        const int dn = (BF16 ? 133 : 24) - kq;  // 33 .. 126 or -14 .. 26
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - dn) << 23);
+#pragma unroll 4
+        for (int k = k0; k < D / 32; k += PER) {
+            float f[8], sum = 0.0f;
+            dims(k, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += f[i];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (t == 0) reinterpret_cast<float*>(to + C::OFF_QS)[(nt * (D / 32) + k) * 8 + gg] = sum * down;
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = (i & 1) ? up * 0.0625f : up;
+                b[i] = pg_pack2<BF16>(f[i] * u, f[i + 4] * u);
+            }
+            dst[k * 32] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+        // the score's factor undoes both
+        if (t == 0 && k0 == 0)
+            reinterpret_cast<float*>(to + C::OFF_F)[nt * 8 + gg] = p.sl2 * __uint_as_float(static_cast<uint32_t>(dn + 127) << 23);
     }
 }
 
