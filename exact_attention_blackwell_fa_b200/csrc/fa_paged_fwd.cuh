@@ -39,7 +39,7 @@
 // that the read-back gives.
 #pragma once
 
-#include <type_traits>
+#include <utility>
 
 #include "fa_paged.cuh"
 
@@ -95,11 +95,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// 16 bytes global -> shared; of the second form only the first `bytes` (0 .. 16) are
-// read, the rest is zero.
+// 16 bytes global -> shared, both at constant offsets; of the second form only the first
+// `bytes` (0 .. 16) are read, the rest is zero.
+template <int TO, int FROM>
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "n"(TO), "n"(FROM)
+                 : "memory");
 }
 __device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, uint32_t bytes)
 {
@@ -335,7 +338,8 @@ struct PagedLoad {
     // the step whose copies come next, and the one after it (its pages on their way):
     // its first token, keys that count, KV head, page of the lane's block of 16 tokens
     int base[2], kmax[2], hkv[2], page[2];
-    long long off[C::MB];  // of the next step's blocks in the pools
+    long long off[C::MB];  // of the next step's blocks in the pools: their rows,
+    int poff[C::MB];       // and from there their pairs
     uint32_t bits;         // which of them have a page
     uint32_t slot, ok;     // shared-memory addresses of this warp's next slot and its page bits
     uint32_t n = 0;        // slot
@@ -377,25 +381,51 @@ struct PagedLoad {
             segment(p);
         }
     }
-    // offset in a slot of the lane's i-th chunk of a block of 16 rows
+    static constexpr int CH = C::RB / 16;  // chunks per row
+    static constexpr bool EVEN = (CH & (CH - 1)) == 0 && CH <= 32;
+    // offset in a slot of the lane's i-th chunk of a block of 16 rows: a part by lane, and
+    // a constant one
     __device__ static uint32_t place(int lane, int i)
     {
-        constexpr int CH = C::RB / 16;  // chunks per row
-        if constexpr ((CH & (CH - 1)) == 0 && CH <= 32) {
-            constexpr int STEP = 32 / CH;  // rows per 32 chunks
+        if constexpr (EVEN) {
             const int r = lane / CH, c = lane % CH;
-            return ((r * C::RBS + ((c ^ C::key(r)) << 4)) ^ (C::key(i * STEP) << 4)) + i * STEP * C::RBS;
+            return (r * C::RBS + ((c ^ C::key(r)) << 4)) ^ (C::key(i * (32 / CH)) << 4);
         } else {
             const int x = lane + 32 * i, r = x / CH, c = x - r * CH;
             return r * C::RBS + ((c ^ C::key(r)) << 4);
         }
     }
+    __host__ __device__ static constexpr int place_more(int i) { return EVEN ? i * (32 / CH) * C::RBS : 0; }
+    template <int MBI, int... I>
+    __device__ static void block_whole(uint32_t dst, const uint8_t* rows, int lane, std::integer_sequence<int, I...>)
+    {
+        (copy16<MBI * 16 * C::RBS + place_more(I), I * 512>(dst + place(lane, I), rows), ...);
+    }
+    template <int... MBI>
+    __device__ void step_whole(const uint8_t* pool, int lane, std::integer_sequence<int, MBI...>)
+    {
+        (block_whole<MBI>(slot, pool + off[MBI], lane, std::make_integer_sequence<int, CH / 2>{}), ...);
+    }
+    // the pairs of all the step's blocks: MB * SCB chunks
+    template <int... I>
+    __device__ void pairs_whole(const uint8_t* pool, int lane, std::integer_sequence<int, I...>)
+    {
+        constexpr int ALL = C::MB * C::SCB;
+        auto from = [&](int i) {
+            const int x = lane + 32 * i, mb = C::SCB % 32 == 0 ? i / (C::SCB / 32) : x / C::SCB;
+            long long o = off[0] + poff[0];
+            if (mb > 0) o = off[C::MB - 1] + poff[C::MB - 1] - C::SCB * 16;
+            return pool + o;
+        };
+        static_assert(C::MB <= 2, "two blocks");
+        ((lane + 32 * I < ALL ? copy16<C::TS * C::RBS + I * 512, I * 512>(slot + lane * 16, from(I)) : void()), ...);
+    }
+
     template <bool VALUE>
     __device__ void issue(const PagedFwdParams& p)
     {
         const int lane = threadIdx.x & 31;
         if (base[0] >= 0) {
-            constexpr int CH = C::RB / 16;
             if constexpr (!VALUE) {
                 const bool good = static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(p.pool.num_pages);
                 bits = __ballot_sync(0xffffffffu, good) & ((1u << C::MB) - 1u);
@@ -403,42 +433,36 @@ struct PagedLoad {
                 // blocks are at least 1280 bytes, so a pool has fewer than 2^32 of them
                 const uint32_t blk = good ? static_cast<uint32_t>(page[0]) * p.pool.Hkv + hkv[0] : 0u;
 #pragma unroll
-                for (int mb = 0; mb < C::MB; ++mb)
-                    off[mb] = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, blk, mb)) * p.block_bytes +
-                              ((base[0] + mb * 16) & (p.pool.page_size - 1)) * C::RB;
+                for (int mb = 0; mb < C::MB; ++mb) {
+                    const int slot0 = (base[0] + mb * 16) & (p.pool.page_size - 1);
+                    off[mb] = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, blk, mb)) * p.block_bytes + slot0 * C::RB;
+                    poff[mb] = p.pool.page_size * C::RB - slot0 * (C::RB - C::SCB);
+                }
                 if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(ok + 4u * n), "r"(bits) : "memory");
             }
-            const uint8_t* const pool = static_cast<const uint8_t*>(VALUE ? p.v_cache : p.k_cache);
-            const bool whole = kmax[0] - base[0] >= C::TS && bits == (1u << C::MB) - 1u;
+            const uint8_t* const pool = static_cast<const uint8_t*>(VALUE ? p.v_cache : p.k_cache) + lane * 16;
+            if (kmax[0] - base[0] >= C::TS && bits == (1u << C::MB) - 1u) {
+                step_whole(pool, lane, std::make_integer_sequence<int, C::MB>{});
+                if constexpr (INT4) pairs_whole(pool, lane, std::make_integer_sequence<int, (C::MB * C::SCB + 31) / 32>{});
+            } else {
+                // only what exists is read; the rest of the slot is zeros
 #pragma unroll
-            for (int mb = 0; mb < C::MB; ++mb) {
-                // 16 rows lie together, and their pairs
-                const uint8_t* const rows = pool + off[mb] + lane * 16;
-                const int slot0 = (base[0] + mb * 16) & (p.pool.page_size - 1);
-                const uint8_t* const pairs = rows + (p.pool.page_size * C::RB - slot0 * (C::RB - C::SCB));
-                const uint32_t dst = slot + mb * 16 * C::RBS;
-                const uint32_t pdst = slot + C::TS * C::RBS + mb * 16 * C::SCB + lane * 16;
-                if (whole) {
-#pragma unroll
-                    for (int i = 0; i < CH / 2; ++i) copy16(dst + place(lane, i), rows + i * 512);
-                    if constexpr (INT4) {
-#pragma unroll
-                        for (int i = 0; i < (C::SCB + 31) / 32; ++i)
-                            if (lane + 32 * i < C::SCB) copy16(pdst + i * 512, pairs + i * 512);
-                    }
-                } else {
-                    // only what exists is read; the rest of the slot is zeros
+                for (int mb = 0; mb < C::MB; ++mb) {
+                    const uint32_t dst = slot + mb * 16 * C::RBS;
+                    const uint8_t* const rows = pool + off[mb];
                     const int valid = (bits >> mb & 1u) ? max(0, min(16, kmax[0] - base[0] - mb * 16)) : 0;
 #pragma unroll
                     for (int i = 0; i < CH / 2; ++i) {
                         const int left = max(0, min(16, valid * C::RB - (lane + 32 * i) * 16));
-                        copy16_part(dst + place(lane, i), left > 0 ? rows + i * 512 : pool, left);
+                        copy16_part(dst + place(lane, i) + place_more(i), left > 0 ? rows + i * 512 : pool, left);
                     }
                     if constexpr (INT4) {
+                        const uint32_t pdst = slot + C::TS * C::RBS + mb * 16 * C::SCB + lane * 16;
 #pragma unroll
                         for (int i = 0; i < (C::SCB + 31) / 32; ++i) {
                             const int left = max(0, min(16, valid * C::SCB - (lane + 32 * i) * 16));
-                            if (lane + 32 * i < C::SCB) copy16_part(pdst + i * 512, left > 0 ? pairs + i * 512 : pool, left);
+                            if (lane + 32 * i < C::SCB)
+                                copy16_part(pdst + i * 512, left > 0 ? rows + poff[mb] + i * 512 : pool, left);
                         }
                     }
                 }
