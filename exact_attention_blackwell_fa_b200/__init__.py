@@ -35,6 +35,7 @@ float32 [batch, Hq, Sq].  A non-OK status raises FAError; nothing falls back.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -486,6 +487,12 @@ def fa_fwd_paged_workspace_size(B: int, max_seqlen_q: int, Hq: int, Hkv: int, d:
     return int(_lib.load().fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d))
 
 
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_size(device_index, B, max_seqlen_q, Hq, Hkv, d) -> int:
+    """fa_fwd_paged_workspace_size on the current device, `device_index`."""
+    return max(256, fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d))
+
+
 def fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q: int,
                  causal: bool = False, scale: float | None = None, out=None, lse=None, workspace=None,
                  stream=None):
@@ -505,20 +512,25 @@ def fa_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_
         raise ValueError(f"fa: the pools hold head_dim {dk}, q has {d}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    for name, t, kind, shape in (("out", out, dtype, q.shape), ("lse", lse, torch.float32, (Hq, total_q))):
-        if t is not None:
-            _check(t, name, kind)
-            _shape(t, name, shape)
-            _same_device(q, **{name: t})
+    if out is not None:
+        _check(out, "out", dtype)
+        _shape(out, "out", q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32)
+        _shape(lse, "lse", (Hq, total_q))
+    if out is not None or lse is not None:
+        _same_device(q, out=out, lse=lse)
     lib = _lib.load()
     with _on(device, stream):
-        out = torch.empty_like(q) if out is None else out
-        lse = q.new_empty((Hq, total_q), dtype=torch.float32) if lse is None else lse
-        need = lib.fa_fwd_paged_workspace_size(B, max_seqlen_q, Hq, Hkv, d)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = q.new_empty((Hq, total_q), dtype=torch.float32)
+        need = _paged_workspace_size(device.index, B, max_seqlen_q, Hq, Hkv, d)
         if workspace is None:
-            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+            workspace = q.new_empty(need, dtype=torch.uint8)
         else:
-            _workspace(workspace, q, need)
+            workspace = _workspace(workspace, q, need)
         code = lib.fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                 lse.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
                                 block_table.data_ptr(), B, max_seqlen_q, total_q, Hq, Hkv, d, page_size,

@@ -127,11 +127,24 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     // no more CTAs than there can be granules
     const long long blocks = (static_cast<long long>(p.max_q) * p.group + C::ROWS - 1) / C::ROWS;
     const long long keys = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
-    const double most = static_cast<double>(p.B) * blocks * p.pool.Hkv * ((keys + C::GR - 1) / C::GR);
+    const double units = static_cast<double>(p.B) * blocks * p.pool.Hkv;
+    const long long granules = (keys + C::GR - 1) / C::GR;
     int grid = C::CTAS * sm_count;
+    // Few short sequences: a unit stays whole, and nothing is left to join.  Up to about
+    // 160 KB of keys and values one CTA takes no longer than the pieces and their join (one
+    // sequence, 8 KV heads, d = 128: 64 / 256 / 384 / 512 tokens 6.2 / 8.6 / 9.7 / 11.4 us
+    // whole, 7.2 / 9.2 / 9.1 / 9.2 us in pieces), and a launch less is 2 us of host time.
+    // 4-bit rows take longer to expand than to read: one or two granules (d = 128, 256
+    // tokens: 9.2 us against 10.2; d = 512: 19.6 against 18.2, 128 tokens 14.7 against 16.2)
+    const bool whole = units <= grid && (INT4 ? granules <= (D <= 256 ? 2 : 1) : keys * 4 * D <= 160 * 1024);
+    fa::PagedFwdParams a = p;
+    a.coarse = whole ? static_cast<int>(granules) : 1;
+    if (whole) a.rec = nullptr;
+    const double most = whole ? units : units * granules;
     if (most < grid) grid = static_cast<int>(most);
-    kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
+    kernel<<<grid, C::THREADS, C::SMEM, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (whole) return FA_OK;
     // the join starts its blocks while the forward's last CTAs run, and waits for them
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -142,7 +155,7 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa::fa_fwd_paged_join_kernel<D, BF16, C::ROWS>, p, grid) == cudaSuccess ? FA_OK
+    return cudaLaunchKernelEx(&cfg, fa::fa_fwd_paged_join_kernel<D, BF16, C::ROWS>, a, grid) == cudaSuccess ? FA_OK
                                                                                                            : FA_ERR_CUDA;
 }
 

@@ -142,6 +142,7 @@ struct PagedFwdParams {
     int B, max_q, total_q, Hq, group, causal;
     float sl2;         // scale * log2(e)
     uint32_t block_bytes;  // of a (page, head)
+    int coarse;        // granules that ranges keep together
     float* opart;      // [2 grid][rows of a unit][D]
     float2* mlpart;    // [2 grid][rows of a unit] (reference maximum, sum)
     PagedRecord* rec;  // [grid]
@@ -194,7 +195,8 @@ struct PagedCfg {
 
 // Lengths of sequence b as the kernels use them.
 struct PagedSeq {
-    int q0, Sq, Sk, nu, kt;
+    int q0, Sq, Sk, nu;
+    int kg, kt;  // granules of a unit, and pieces of `coarse` granules that ranges are cut from
 };
 template <class C>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedFwdParams& p, int b)
@@ -205,7 +207,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedFwdParams& p, int b)
     s.Sq = s.q0 >= 0 && end <= p.total_q && end > s.q0 ? static_cast<int>(min(end - s.q0, static_cast<long long>(p.max_q))) : 0;
     s.Sk = max(0, min(p.seqlens_k[b], p.pool.max_pages << p.pool.page_shift));
     s.nu = static_cast<int>((static_cast<long long>(s.Sq) * p.group + C::ROWS - 1) / C::ROWS) * p.pool.Hkv;
-    s.kt = s.Sk > 0 ? (s.Sk - 1) / C::GR + 1 : 1;
+    s.kg = s.Sk > 0 ? (s.Sk - 1) / C::GR + 1 : 1;
+    s.kt = p.coarse > 1 ? (s.kg - 1) / p.coarse + 1 : s.kg;
     return s;
 }
 
@@ -278,6 +281,8 @@ __device__ __forceinline__ void paged_start(const PagedFwdParams& p, PagedStart*
 struct PagedSegment {
     PagedSeq s;
     int b, u, g0, g1;
+    int first, last;  // whether it begins and ends its unit
+    int left;         // the unit's pieces past it
     int r0, R;     // first row of the unit, rows of the sequence
     int kmax;      // keys that some row of the unit sees
 };
@@ -307,8 +312,12 @@ struct PagedWalk {
         x.s = s;
         x.b = b;
         x.u = u;
-        x.g0 = g;
-        x.g1 = static_cast<int>(min(static_cast<long long>(s.kt), g + left));
+        const int end = static_cast<int>(min(static_cast<long long>(s.kt), g + left));
+        x.g0 = g * p.coarse;
+        x.g1 = min(s.kg, end * p.coarse);
+        x.first = g == 0;
+        x.last = end == s.kt;
+        x.left = s.kt - end;
         x.r0 = (u / p.pool.Hkv) * C::ROWS;
         x.R = s.Sq * p.group;
         x.kmax = s.Sk;
@@ -316,8 +325,8 @@ struct PagedWalk {
             const int last = (min(x.r0 + C::ROWS, x.R) - 1) / p.group;
             x.kmax = max(0, min(s.Sk, last + s.Sk - s.Sq + 1));
         }
-        left -= x.g1 - x.g0;
-        g = x.g1;
+        left -= end - g;
+        g = end;
         if (g == s.kt) {
             g = 0;
             ++u;
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     paged_start<C>(p, &start, red);
-    if (threadIdx.x == 0) p.rec[blockIdx.x].last = -1;
+    if (threadIdx.x == 0 && p.rec != nullptr) p.rec[blockIdx.x].last = -1;
     if (start.lo >= start.hi) return;
 
     const uint32_t ring = sbase + C::OFF_RING + w * C::NST * C::SLOT;
@@ -729,6 +738,14 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     }
                 }
             }
+            // ---- the scale, in base 2.  Rounded here, once: a difference to the rounded maximum
+            // is then never above the true one's sign, however large the scores are
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[mb][nt][i] *= f[nt][i & 1];
             // ---- masks: causal limits, the sequence's end, tokens without a page
             const bool whole = (bits & ((1u << MB) - 1u)) == (1u << MB) - 1u;
             if (base > lim0 - C::TS || !whole) {
@@ -758,7 +775,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[nt][i] = v * f[nt][i];
+                    mx[nt][i] = v;
                     grow |= mx[nt][i] > m[nt][i] + 8.0f;
                 }
             // the reference maximum moves (and O and l with it) only when a score exceeds it
@@ -792,7 +809,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float ref = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
-                            v[i] = ex2_sfu(fmaf(s[mb][nt][2 * y + i], f[nt][i], -ref));
+                            v[i] = ex2_sfu(s[mb][nt][2 * y + i] - ref);
                             l[nt][i] += v[i];
                         }
                         const uint32_t hi = pg_pack2<BF16>(v[0], v[1]);
@@ -899,8 +916,8 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     o[mt][nt][2 + i] *= al;
                 }
             }
-        const bool whole = x.g0 == 0 && x.g1 == x.s.kt;
-        const size_t piece = (2 * static_cast<size_t>(blockIdx.x) + (x.g0 == 0 ? 1 : 0)) * C::ROWS;
+        const bool whole = x.first && x.last;
+        const size_t piece = (2 * static_cast<size_t>(blockIdx.x) + (x.first ? 1 : 0)) * C::ROWS;
         const int h0 = (x.u % p.pool.Hkv) * p.group;
         float* buf = reinterpret_cast<float*>(smem + C::OFF_RED);
 #pragma unroll
@@ -935,11 +952,11 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 #pragma unroll
                     for (int ww = 0; ww < C::W; ++ww) {
                         const float2 z = ml[ww * C::ROWS + nt * 8 + rr];
-                        if (z.x != -INFINITY) sum += z.y * ex2_sfu(z.x - top);
+                        if (z.y != 0.0f) sum += z.y * ex2_sfu(z.x - top);  // a NaN stays one
                     }
                     if (whole) {
                         const int tok = r / p.group, h = h0 + r - tok * p.group;
-                        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) acc[i] *= inv;
                         reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
@@ -947,7 +964,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                             pg_pack8<BF16>(acc);
                         if (part == 0 && v == 0)
                             p.lse[static_cast<size_t>(h) * p.total_q + x.s.q0 + tok] =
-                                sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                                sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
                     } else {
                         float4* dst = reinterpret_cast<float4*>(p.opart + (piece + nt * 8 + rr) * D + part * C::DP + v * 8);
                         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -957,9 +974,9 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                 }
             }
         }
-        if (!whole && x.g0 == 0 && threadIdx.x == 0) {
+        if (!whole && x.first && threadIdx.x == 0) {
             // the pieces that follow are in the ranges up to the one that holds the unit's end
-            const long long end = start.hi + (x.s.kt - x.g1);
+            const long long end = start.hi + x.left;
             const long long last = (end * gridDim.x + start.total - 1) / start.total - 1;
             p.rec[blockIdx.x] = PagedRecord{x.b, x.u, static_cast<int>(last), 0, start.total};
         }
@@ -994,7 +1011,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
         if (rec.total * j / grid == rec.total * (j + 1) / grid) continue;  // an empty range
         const size_t piece = (2 * static_cast<size_t>(j) + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * ROWS + blockIdx.y;
         const float2 z = p.mlpart[piece];
-        if (z.x == -INFINITY) continue;
+        if (z.y == 0.0f) continue;
         const float mn = fmaxf(m, z.x), a = ex2_sfu(m - mn), b = ex2_sfu(z.x - mn);
         m = mn;
         l = l * a + z.y * b;
@@ -1011,10 +1028,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
     for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, ml[i].x);
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) {
-        f[i] = ml[i].x == -INFINITY ? 0.0f : ex2_sfu(ml[i].x - top);
+        f[i] = ml[i].y == 0.0f ? 0.0f : ex2_sfu(ml[i].x - top);
         sum += ml[i].y * f[i];
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int tok = r / p.group, h = (rec.u % p.pool.Hkv) * p.group + r - tok * p.group;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (static_cast<size_t>(q0 + tok) * p.Hq + h) * D);
     for (int c = threadIdx.x; c < D / 2; c += kJoinWarps * 32) {
@@ -1028,7 +1045,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
     }
     if (threadIdx.x == 0)
         p.lse[static_cast<size_t>(h) * p.total_q + q0 + tok] =
-            sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

@@ -534,6 +534,119 @@ def test_paged_forward_sharp_scores_and_large_values(int4):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("d", [128, 192, 256, 384, 512])
+def test_paged_forward_every_head_dim_and_row_count(d, dt, int4):
+    """One, two and four tiles of eight rows (and several blocks of them), short sequences
+    kept whole and long ones cut into pieces, for every head dim, type and pool."""
+    fa = fa_mod()
+    Hq, Hkv, page = 10, 2, 64                                        # groups of 5
+    for news, lens in (([1, 1], [70, 33]), ([3, 1], [300, 1200]), ([2, 6], [900, 17]), ([11], [513])):
+        c = Cache(lens, Hkv, d, page, int4, dt, seed=d)
+        rows = c.fill(lens, seed=d + 1)
+        q = randn(sum(news), Hq, d, seed=d + 2, dt=dt)
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu_of(news), i32(lens), c.table, max(news), causal=True)
+        status_ok(fa)
+        check_paged(c, rows, q, news, lens, True, d ** -0.5, o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("int4", [False, True])
+def test_paged_forward_many_sequences(int4):
+    """More sequences than a block has threads, some without queries, some without keys."""
+    fa = fa_mod()
+    B, Hq, Hkv, d, dt = 700, 4, 1, 128, BF16
+    lens = [(37 * b) % 151 for b in range(B)]
+    news = [(b % 5 != 0) + (b % 7 == 0) for b in range(B)]
+    lens[650] = 3000
+    c = Cache(lens, Hkv, d, 16, int4, dt)
+    rows = c.fill(lens, seed=1)
+    q = randn(sum(news), Hq, d, seed=2, dt=dt)
+    o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu_of(news), i32(lens), c.table, max(news), causal=True)
+    status_ok(fa)
+    check_paged(c, rows, q, news, lens, True, d ** -0.5, o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_paged_forward_query_magnitudes(dt):
+    """4-bit pools scale each query row by a power of two: rows of zeros, of tiny and of
+    large values, side by side in one tile."""
+    fa = fa_mod()
+    lens, d = [400], 128
+    c = Cache(lens, 1, d, 32, True, dt)
+    rows = c.fill(lens, seed=1)
+    e = [0.0, 1.0, 2.0 ** -12, 2.0 ** 10, 2.0 ** -20 if dt == FP16 else 2.0 ** -100, 2.0 ** 13 if dt == FP16 else 2.0 ** 30]
+    q = randn(1, len(e), d, seed=2, dt=dt).clamp(-3, 3) * torch.tensor(e, device="cuda").to(dt)[None, :, None]
+    for scale in (d ** -0.5, 1e-5, 2.0 ** -40):
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 1]), i32(lens), c.table, 1, scale=scale)
+        status_ok(fa)
+        # rows whose scores the definition's own softmax cannot tell apart in 32 bits are left out
+        sizes = (torch.einsum("ihd,jhd->hij", q.double().abs(), rows[0][0].abs().expand(-1, len(e), -1)).amax(-1)[:, 0] * scale)
+        fine = (sizes < 1e3).nonzero()[:, 0]
+        assert fine.numel() >= 3 and o.isfinite().all()
+        check_paged(c, rows, q[:, fine], [1], lens, False, scale, o[:, fine], lse[fine])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("int4", [False, True])
+def test_a_nan_stays_in_its_sequence(int4):
+    """A NaN among a sequence's visible keys or values makes that sequence's outputs NaN
+    and no other's; one past its end or behind the causal limit does nothing."""
+    fa = fa_mod()
+    lens, news, d, dt = [50, 700, 60], [1, 1, 2], 128, BF16
+    for n in (49, 699, 3):                      # in a whole sequence, in a cut one's last piece
+        for which in ("k", "v"):
+            c = Cache(lens, 1, d, 16, int4, dt)
+            k, v = randn(sum(lens), 1, d, seed=1), randn(sum(lens), 1, d, seed=2)
+            b = 1 if n == 699 else 0
+            at = sum(lens[:b]) + n
+            (k if which == "k" else v)[at] = NAN
+            fa.fa_kv_append(None, k, v, c.k, c.v, cu_of(lens), i32(lens), c.table)
+            q = randn(sum(news), 4, d, seed=3)
+            o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu_of(news), i32(lens), c.table, 2, causal=True)
+            status_ok(fa)
+            assert o[b].isnan().all() and o[[i for i in range(4) if i != b]].isfinite().all()
+            assert lse[:, b].isnan().all() == (which == "k")
+            assert lse[:, [i for i in range(4) if i != b]].isfinite().all()
+            cut = list(lens)
+            cut[b] = n                          # the NaN is the first token past the end
+            if n:
+                o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu_of(news), i32(cut), c.table, 2, causal=True)
+                status_ok(fa)
+                assert o.isfinite().all() and lse.isfinite().all()
+
+
+@pytest.mark.gpu
+def test_explicit_streams_and_two_calls_at_once():
+    """stream= as a torch stream and as a raw handle; two calls in flight on two streams."""
+    fa = fa_mod()
+    lens, d, Hq = [3000, 500], 128, 8
+    c = Cache(lens, 2, d, 16, False, BF16)
+    c.fill(lens, seed=1)
+    cu, sk = i32([0, 1, 2]), i32(lens)
+    qs = [randn(2, Hq, d, seed=s) for s in (2, 3)]
+    want = [fa.fa_fwd_paged(q, c.k, c.v, cu, sk, c.table, 1) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(5):
+        got = [fa.fa_fwd_paged(q, c.k, c.v, cu, sk, c.table, 1, stream=s if rep % 2 else s.cuda_stream)
+               for q, s in zip(qs, streams)]
+        k, v = fa.fa_kv_gather(c.k, c.v, cu_of(lens), c.table, sum(lens), stream=streams[0])
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ref = torch.cat([c.rows(c.k, b, n) for b, n in enumerate(lens)])
+    assert torch.equal(k.double(), ref)
+    x = randn(2, 2, d, seed=5)
+    fa.fa_kv_append(None, x, x, c.k, c.v, cu, sk, c.table, stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(c.rows(c.v, 0, 3000)[-1], x[0].double())
+    status_ok(fa)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("int4", [False, True])
 def test_bad_pages_are_left_out_and_reported(int4):
     """Entries that are no pages: nothing is written for them, they read as zeros, take no
     part in attention, and the device status says so."""
