@@ -150,12 +150,15 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, C::ROWS);
+    // a block per cut unit; where pieces per unit are many, or blocks few, a block per row
+    // of it (b = 1, 1000 tokens, 8 KV heads: 10.4 us against 12.2 in all; 64 sequences up to
+    // 8192 tokens, 4 KV heads: 94.3 us with a block per row, 91.2 with one)
+    cfg.gridDim = dim3(grid, units * 8 < grid || grid * C::ROWS <= 1024 ? C::ROWS : 1);
     cfg.blockDim = dim3(fa::kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa::fa_fwd_paged_join_kernel<D, BF16, C::ROWS>, a, grid) == cudaSuccess ? FA_OK
+    return cudaLaunchKernelEx(&cfg, fa::fa_fwd_paged_join_kernel<D, BF16, C::ROWS>, a) == cudaSuccess ? FA_OK
                                                                                                            : FA_ERR_CUDA;
 }
 

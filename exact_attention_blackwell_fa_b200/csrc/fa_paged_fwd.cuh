@@ -125,11 +125,10 @@ __device__ __forceinline__ T lds(const uint8_t* a)
 // Parameters
 // ---------------------------------------------------------------------------------
 // A unit that was cut: its pieces are slot 2 i + 1 of the CTA i that writes the record
-// and slots 2 j of the CTAs i < j <= last whose range is not empty.
+// and slots 2 j of the CTAs i < j <= last (a sum of 0 where a range was empty).
 struct PagedRecord {
     int b, u, last;  // last < 0: nothing to join
     int pad;
-    long long total;
 };
 
 struct PagedFwdParams {
@@ -584,7 +583,11 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
 
     paged_start<C>(p, &start, red);
     if (threadIdx.x == 0 && p.rec != nullptr) p.rec[blockIdx.x].last = -1;
-    if (start.lo >= start.hi) return;
+    if (start.lo >= start.hi) {
+        if (p.rec != nullptr && threadIdx.x < C::ROWS)
+            p.mlpart[2 * static_cast<size_t>(blockIdx.x) * C::ROWS + threadIdx.x] = make_float2(-INFINITY, 0.0f);
+        return;
+    }
 
     const uint32_t ring = sbase + C::OFF_RING + w * C::NST * C::SLOT;
     const uint32_t okw = sbase + C::OFF_OK + w * 32;
@@ -978,20 +981,65 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             // the pieces that follow are in the ranges up to the one that holds the unit's end
             const long long end = start.hi + x.left;
             const long long last = (end * gridDim.x + start.total - 1) / start.total - 1;
-            p.rec[blockIdx.x] = PagedRecord{x.b, x.u, static_cast<int>(last), 0, start.total};
+            p.rec[blockIdx.x] = PagedRecord{x.b, x.u, static_cast<int>(last), 0};
         }
     }
     copy_wait<0>();
 }
 
 // ---------------------------------------------------------------------------------
-// Joins the pieces of the units that were cut: one block per (record, row), its warps
-// taking the pieces in turn; the order of every sum is fixed.
+// Joins the pieces of the units that were cut.  A block has one record; with few pieces
+// each warp joins rows of its own, with many the warps of the block share a row's.  The
+// order of every sum is fixed by the pieces' number.
 // ---------------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
+constexpr int kJoinFew = 16;
+
+// Adds pieces first, first + step, .. of a row; lane's dims lane + 32 c.
+template <int D, int ROWS>
+__device__ __forceinline__ void join_pieces(const PagedFwdParams& p, int last, int row, int first, int step,
+                                            float (&acc)[D / 32], float& m, float& l)
+{
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] = 0.0f;
+    for (int j0 = first; j0 <= last; j0 += 32 * step) {  // 32 pieces' statistics at a time
+        auto piece = [&](int j) {
+            return (2 * static_cast<size_t>(j) + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * ROWS + row;
+        };
+        const int j = j0 + lane * step;
+        float2 z = make_float2(-INFINITY, 0.0f);
+        if (j <= last) z = p.mlpart[piece(j)];
+        float mn = z.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mn = fmaxf(mn, m);
+        const float a = l == 0.0f ? 0.0f : ex2_sfu(m - mn);
+        const float b = z.y == 0.0f ? 0.0f : ex2_sfu(z.x - mn);
+        float sum = z.y * b;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        m = mn;
+        l = l * a + sum;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[c] *= a;
+        const uint32_t some = __ballot_sync(0xffffffffu, z.y != 0.0f);
+        const int n = min(32, (last - j0) / step + 1);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            if (!(some >> i & 1u)) continue;  // nothing was written
+            const float f = __shfl_sync(0xffffffffu, b, i);
+            const float* src = p.opart + piece(j0 + i * step) * D + lane;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(src[32 * c], f, acc[c]);
+        }
+    }
+}
 
 template <int D, bool BF16, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(const __grid_constant__ PagedFwdParams p, int grid)
+__global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(const __grid_constant__ PagedFwdParams p)
 {
     __shared__ float part[kJoinWarps][D];
     __shared__ float2 ml[kJoinWarps];
@@ -1001,51 +1049,48 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q0 = p.cu_q[rec.b];
     const int Sq = max(0, min(p.cu_q[rec.b + 1] - q0, p.max_q));
-    const int r = (rec.u / p.pool.Hkv) * ROWS + blockIdx.y;
-    if (r >= Sq * p.group) return;
-    constexpr int PER = D / 32;
-    float acc[PER], m = -INFINITY, l = 0.0f;
+    const int r0 = (rec.u / p.pool.Hkv) * ROWS, rows = min(ROWS, Sq * p.group - r0);
+    const int h0 = (rec.u % p.pool.Hkv) * p.group;
+    float acc[D / 32], m, l;
+    const bool few = gridDim.y == 1 && rec.last - static_cast<int>(blockIdx.x) < kJoinFew;
+    for (int row = few ? w : blockIdx.y; row < rows; row += few ? kJoinWarps : gridDim.y) {
+        const int tok = (r0 + row) / p.group, h = h0 + r0 + row - tok * p.group;
+        uint16_t* const dst = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(q0 + tok) * p.Hq + h) * D;
+        float* const lse = p.lse + static_cast<size_t>(h) * p.total_q + q0 + tok;
+        if (few) {
+            join_pieces<D, ROWS>(p, rec.last, row, blockIdx.x, 1, acc, m, l);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = 0.0f;
-    for (int j = blockIdx.x + w; j <= rec.last; j += kJoinWarps) {
-        if (rec.total * j / grid == rec.total * (j + 1) / grid) continue;  // an empty range
-        const size_t piece = (2 * static_cast<size_t>(j) + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * ROWS + blockIdx.y;
-        const float2 z = p.mlpart[piece];
-        if (z.y == 0.0f) continue;
-        const float mn = fmaxf(m, z.x), a = ex2_sfu(m - mn), b = ex2_sfu(z.x - mn);
-        m = mn;
-        l = l * a + z.y * b;
-        const float* src = p.opart + piece * D + lane;
+            for (int c = 0; c < D / 32; ++c) dst[lane + 32 * c] = static_cast<uint16_t>(pg_pack2<BF16>(acc[c] * inv, 0.0f));
+            if (lane == 0) *lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            continue;
+        }
+        join_pieces<D, ROWS>(p, rec.last, row, blockIdx.x + w, kJoinWarps, acc, m, l);
+        __syncthreads();  // the last row's parts are done with
 #pragma unroll
-        for (int c = 0; c < PER; ++c) acc[c] = acc[c] * a + src[32 * c] * b;
-    }
+        for (int c = 0; c < D / 32; ++c) part[w][lane + 32 * c] = acc[c];
+        if (lane == 0) ml[w] = make_float2(m, l);
+        __syncthreads();
+        float top = -INFINITY, sum = 0.0f, f[kJoinWarps];
 #pragma unroll
-    for (int c = 0; c < PER; ++c) part[w][lane + 32 * c] = acc[c];
-    if (lane == 0) ml[w] = make_float2(m, l);
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f, f[kJoinWarps];
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, ml[i].x);
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-        f[i] = ml[i].y == 0.0f ? 0.0f : ex2_sfu(ml[i].x - top);
-        sum += ml[i].y * f[i];
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int tok = r / p.group, h = (rec.u % p.pool.Hkv) * p.group + r - tok * p.group;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (static_cast<size_t>(q0 + tok) * p.Hq + h) * D);
-    for (int c = threadIdx.x; c < D / 2; c += kJoinWarps * 32) {
-        float a = 0.0f, b = 0.0f;
+        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, ml[i].x);
 #pragma unroll
         for (int i = 0; i < kJoinWarps; ++i) {
-            a = fmaf(f[i], part[i][2 * c], a);
-            b = fmaf(f[i], part[i][2 * c + 1], b);
+            f[i] = ml[i].y == 0.0f ? 0.0f : ex2_sfu(ml[i].x - top);
+            sum += ml[i].y * f[i];
         }
-        dst[c] = pg_pack2<BF16>(a * inv, b * inv);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int c = threadIdx.x; c < D / 2; c += kJoinWarps * 32) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) {
+                a = fmaf(f[i], part[i][2 * c], a);
+                b = fmaf(f[i], part[i][2 * c + 1], b);
+            }
+            reinterpret_cast<uint32_t*>(dst)[c] = pg_pack2<BF16>(a * inv, b * inv);
+        }
+        if (threadIdx.x == 0) *lse = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
     }
-    if (threadIdx.x == 0)
-        p.lse[static_cast<size_t>(h) * p.total_q + q0 + tok] =
-            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace fa
