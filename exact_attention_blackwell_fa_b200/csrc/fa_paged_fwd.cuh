@@ -565,6 +565,98 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
 }
 
 // ---------------------------------------------------------------------------------
+// The second product where its tokens' values are not finite and not every row sees
+// them: a token at a time, only what a row sees.  Rare; kept out of the way of the rest.
+// ---------------------------------------------------------------------------------
+// The mma row of a score tile that holds token (row & 7): at the narrowest rows the
+// tokens are dealt so that the value loads of a warp meet no bank twice.
+template <bool INT4, class C>
+__device__ __forceinline__ int token_of_slot(int slot)
+{
+    return C::RBS == 64 && INT4 ? (slot & ~3) | ((slot & 1) << 1) | ((slot >> 1) & 1) : slot;
+}
+
+// Whether a slot's values (4-bit: scales and zeros) hold an infinity or a NaN.
+template <int D, bool BF16, bool INT4, class C>
+__device__ __forceinline__ bool paged_slot_bad(const uint8_t* vs)
+{
+    constexpr int BYTES = INT4 ? C::TS * C::SCB : C::TS * C::RBS;
+    constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u;
+    const uint8_t* const from = INT4 ? vs + C::TS * C::RBS : vs;
+    bool bad = false;
+#pragma unroll 1
+    for (int i = (threadIdx.x & 31) * 4; i < BYTES; i += 128) {
+        const uint32_t w = lds<uint32_t>(from + i);
+        bad |= (w & EXP) == EXP || (w >> 16 & EXP) == EXP;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+template <int D, bool BF16, bool INT4, int NT, class C>
+__device__ __forceinline__ void paged_product_by_token(const uint8_t* vs, int base, uint32_t bits, const int (&lim)[NT][2],
+                                                       const uint32_t (&ph)[C::MB][NT][2],
+                                                       const uint32_t (&pl)[C::MB][NT][2], float (&o)[D / 16][NT][4])
+{
+    const int lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int k = 0; k < C::TS; ++k) {
+        const int mb = k >> 4, row = mb * 16 + (k & 8) + token_of_slot<INT4, C>(k & 7);
+        float w[NT][2];
+        bool sees[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint32_t hi = (k & 8) ? ph[0][nt][1] : ph[0][nt][0], lo = (k & 8) ? pl[0][nt][1] : pl[0][nt][0];
+            if (C::MB == 2 && mb) {
+                hi = (k & 8) ? ph[C::MB - 1][nt][1] : ph[C::MB - 1][nt][0];
+                lo = (k & 8) ? pl[C::MB - 1][nt][1] : pl[C::MB - 1][nt][0];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // the weight of column 2 t + i lies with the lane that feeds it to the product
+                const int from = (2 * t + i) * 4 + ((k & 7) >> 1);
+                const float2 a = pg_unpack2<BF16>(__shfl_sync(0xffffffffu, hi, from));
+                const float2 b = pg_unpack2<BF16>(__shfl_sync(0xffffffffu, lo, from));
+                w[nt][i] = (k & 1) ? a.y + b.y : a.x + b.x;
+                sees[nt][i] = (bits >> mb & 1u) && base + row < lim[nt][i];
+            }
+        }
+        auto add = [&](int mt, float u, float v) {  // dims of the lane's rows of tile mt
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (sees[nt][i]) {
+                        o[mt][nt][i] = fmaf(w[nt][i], u, o[mt][nt][i]);
+                        o[mt][nt][2 + i] = fmaf(w[nt][i], v, o[mt][nt][2 + i]);
+                    }
+        };
+        if constexpr (!INT4) {
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                const uint8_t* const at = vs + row * C::RBS + gg * 2;
+                const uint16_t u = lds<uint16_t>(at + (((2 * mt) ^ C::key(row)) << 4));
+                const uint16_t v = lds<uint16_t>(at + (((2 * mt + 1) ^ C::key(row)) << 4));
+                add(mt, pg_unpack2<BF16>(u).x, pg_unpack2<BF16>(v).x);
+            }
+        } else {
+#pragma unroll
+            for (int ws = 0; ws < D / 64; ++ws) {
+                const int c = 2 * ws + (gg >> 2);
+                const uint32_t word = lds<uint32_t>(vs + row * C::RBS + ((c ^ C::key(row)) << 4) + (gg & 3) * 4);
+                const float2 sz = pg_unpack2<BF16>(lds<uint32_t>(vs + C::TS * C::RBS + row * C::SCB + c * 4));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float u = fmaf(static_cast<float>(word >> (4 * j) & 15u), sz.x, sz.y);
+                    const float v = fmaf(static_cast<float>(word >> (16 + 4 * j) & 15u), sz.x, sz.y);
+                    const float2 r = pg_unpack2<BF16>(pg_pack2<BF16>(u, v));
+                    add(ws * 4 + j, r.x, r.y);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------
 template <int D, bool BF16, bool INT4, int NT>
@@ -608,11 +700,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         }
     };
 
-    // the mma row of a score tile that holds token (row & 7): at the narrowest rows the
-    // tokens are dealt so that the value loads of a warp meet no bank twice
-    auto tok_of = [](int slot) {
-        return C::RBS == 64 && INT4 ? (slot & ~3) | ((slot & 1) << 1) | ((slot >> 1) & 1) : slot;
-    };
+    auto tok_of = [](int slot) { return token_of_slot<INT4, C>(slot); };
     const int row_a = tok_of(gg);
     // offsets in a slot of the lane's key words (rows row_a, row_a + 8) and value words
     // (rows v_row, the next slot's token, and both + 8)
@@ -827,7 +915,13 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             const uint32_t vat = at;
             const uint8_t* const vs = smem + vat;
             turn();
-            if constexpr (!INT4) {
+            // Where some rows see a token and others do not, an infinity or a NaN among its
+            // values must not meet the others' weight of 0 in a product
+            bool plain = true;
+            if (base > lim0 - C::TS && lim0 < x.kmax) plain = !paged_slot_bad<D, BF16, INT4, C>(vs);
+            if (!plain) {
+                paged_product_by_token<D, BF16, INT4, NT, C>(vs, base, bits, lim, ph, pl, o);
+            } else if constexpr (!INT4) {
                 const int r = (lane & 7) + ((lane >> 4) << 3);
                 const uint32_t row = sbase + vat + r * C::RBS;
 #pragma unroll

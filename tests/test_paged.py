@@ -618,6 +618,41 @@ def test_a_nan_stays_in_its_sequence(int4):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("d,group,dt", [(128, 4, BF16), (128, 1, FP16), (256, 3, FP16), (512, 2, BF16), (192, 8, BF16)])
+def test_non_finite_values_behind_the_causal_limit(d, group, dt, int4):
+    """A token's infinity or NaN, in its key or its values, reaches the queries that see it
+    and none before it."""
+    fa = fa_mod()
+    news, n = [4], 70
+    for at, bad in ((69, NAN), (68, math.inf), (67, NAN), (66, -math.inf)):  # the last new tokens
+        for which in ("k", "v"):
+            c = Cache([n], 1, d, 16, int4, dt)
+            k, v = randn(n, 1, d, seed=1, dt=dt), randn(n, 1, d, seed=2, dt=dt)
+            (k if which == "k" else v)[at, 0, 5] = bad
+            q = randn(4, group, d, seed=3, dt=dt).abs() + 0.5
+            fa.fa_kv_append(None, k, v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+            o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 4]), i32([n]), c.table, 4, causal=True)
+            status_ok(fa)
+            first = at - (n - 4)                 # the first query that sees it
+            rows = [(c.rows(c.k, 0, n), c.rows(c.v, 0, n))]
+            assert o[:first].isfinite().all() and lse[:, :first].isfinite().all()
+            if first:
+                clean = [(r[0][: n - 4 + first], r[1][: n - 4 + first]) for r in rows]
+                check_paged(c, clean, q[:first], [first], [n - 4 + first], True, d ** -0.5, o[:first], lse[:, :first])
+            seen = o[first:]
+            if which == "v":                     # only the dims that hold it (4 bits: their group)
+                dims = torch.zeros(d, dtype=torch.bool, device="cuda")
+                dims[0 if int4 else 5: 32 if int4 else 6] = True
+                want = torch.tensor(NAN if int4 else bad)
+                got = seen[..., dims].float()
+                assert got.isnan().all() if want.isnan() else (got == want.item()).all()
+                assert seen[..., ~dims].isfinite().all() and lse.isfinite().all()
+            elif int4 or bad != -math.inf:       # (a score of -inf takes no part)
+                assert seen.isnan().all() and not lse[:, first:].isfinite().any()
+
+
+@pytest.mark.gpu
 def test_explicit_streams_and_two_calls_at_once():
     """stream= as a torch stream and as a raw handle; two calls in flight on two streams."""
     fa = fa_mod()
