@@ -324,6 +324,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     p.total_q = total_q;
     p.Hq = Hq;
     p.group = Hq / Hkv;
+    p.by_group = fa::Divider::by(p.group);
+    p.by_hkv = fa::Divider::by(Hkv);
     p.causal = causal ? 1 : 0;
     p.sl2 = scale * 1.4426950408889634f;
     const bool bf16 = dt == FA_BF16, int4 = fmt == FA_KV_INT4;

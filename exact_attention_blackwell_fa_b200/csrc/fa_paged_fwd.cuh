@@ -124,6 +124,23 @@ __device__ __forceinline__ T lds(const uint8_t* a)
 // ---------------------------------------------------------------------------------
 // Parameters
 // ---------------------------------------------------------------------------------
+// Division of 0 .. 2^31 - 1 by a number that a launch knows: with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + (n m >> 32)) >> s.
+struct Divider {
+    uint32_t d, m, s;
+    __host__ static Divider by(uint32_t d)
+    {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        return {d, static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+    }
+    __device__ __forceinline__ int quotient(int n) const
+    {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s);
+    }
+    __device__ __forceinline__ int remainder(int n) const { return n - quotient(n) * static_cast<int>(d); }
+};
+
 // A unit that was cut: its pieces are slot 2 i + 1 of the CTA i that writes the record
 // and slots 2 j of the CTAs i < j <= last (a sum of 0 where a range was empty).
 struct PagedRecord {
@@ -139,6 +156,7 @@ struct PagedFwdParams {
     const int *cu_q, *seqlens_k;
     PoolView pool;
     int B, max_q, total_q, Hq, group, causal;
+    Divider by_group, by_hkv;
     float sl2;         // scale * log2(e)
     uint32_t block_bytes;  // of a (page, head)
     int coarse;        // granules that ranges keep together
@@ -224,6 +242,13 @@ __device__ __forceinline__ long long block_sum(long long x, long long* red)
     return s;
 }
 
+// n / d, by 32 bits where they do
+__device__ __forceinline__ long long divide(long long n, long long d)
+{
+    if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
 // Where a CTA's range of granules begins: sequence b, granule `at` of its nu * kt.
 struct PagedStart {
     int b;
@@ -245,7 +270,7 @@ __device__ __forceinline__ void paged_start(const PagedFwdParams& p, PagedStart*
         for (int b = tid; b < p.B; b += T)
             if (p.seqlens_k[b] > (p.pool.max_pages << p.pool.page_shift)) record_bad_page(PAGED_FWD);
     const long long total = block_sum(mine, red);
-    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    const long long lo = divide(total * blockIdx.x, gridDim.x), hi = divide(total * (blockIdx.x + 1), gridDim.x);
     if (tid == 0) *out = PagedStart{0, 0, lo, hi, total};
     long long before = 0;
     for (int c = 0; c < p.B && before <= lo; c += T) {  // T sequences at a time: an inclusive sum over the block
@@ -297,7 +322,7 @@ struct PagedWalk {
         left = st.hi - st.lo;
         if (left <= 0) return;
         s = paged_seq<C>(p, b);
-        u = static_cast<int>(st.at / s.kt);
+        u = static_cast<int>(divide(st.at, s.kt));
         g = static_cast<int>(st.at - static_cast<long long>(u) * s.kt);
     }
     __device__ bool next(const PagedFwdParams& p, PagedSegment& x)
@@ -317,11 +342,11 @@ struct PagedWalk {
         x.first = g == 0;
         x.last = end == s.kt;
         x.left = s.kt - end;
-        x.r0 = (u / p.pool.Hkv) * C::ROWS;
+        x.r0 = p.by_hkv.quotient(u) * C::ROWS;
         x.R = s.Sq * p.group;
         x.kmax = s.Sk;
         if (p.causal) {
-            const int last = (min(x.r0 + C::ROWS, x.R) - 1) / p.group;
+            const int last = p.by_group.quotient(min(x.r0 + C::ROWS, x.R) - 1);
             x.kmax = max(0, min(s.Sk, last + s.Sk - s.Sq + 1));
         }
         left -= end - g;
@@ -366,7 +391,7 @@ struct PagedLoad {
         more = walk.next(p, seg);
         if (!more) return;
         g = seg.g0;
-        h = seg.u % p.pool.Hkv;
+        h = p.by_hkv.remainder(seg.u);
         table = p.pool.table + static_cast<size_t>(seg.b) * p.pool.max_pages;
     }
     // the warp's next step into entry i; base < 0: none is left
@@ -500,13 +525,13 @@ __device__ __forceinline__ void paged_stage_q(const PagedFwdParams& p, const Pag
 {
     using C = PagedCfg<D, INT4, NT>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
-    const int h0 = (x.u % p.pool.Hkv) * p.group;
+    const int h0 = p.by_hkv.remainder(x.u) * p.group;
     // the warps of a tile share its blocks of 32 dims
     static_assert(C::W % NT == 0, "warps per tile");
     constexpr int PER = C::W / NT;
     const int nt = w % NT, k0 = w / NT;
     const int r = x.r0 + nt * 8 + gg;
-    const int tok = r / p.group;
+    const int tok = p.by_group.quotient(r);
     const bool ok = r < x.R;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) +
                           (static_cast<size_t>(x.s.q0 + (ok ? tok : 0)) * p.Hq + h0 + (ok ? r - tok * p.group : 0)) * D;
@@ -734,10 +759,10 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                 l[nt][i] = 0.0f;
                 const int r = x.r0 + nt * 8 + 2 * t + i;
                 f[nt][i] = INT4 ? reinterpret_cast<const float*>(sq + C::OFF_F)[nt * 8 + 2 * t + i] : p.sl2;
-                lim[nt][i] = p.causal && r < x.R ? min(x.s.Sk, r / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;
+                lim[nt][i] = p.causal && r < x.R ? min(x.s.Sk, p.by_group.quotient(r) + x.s.Sk - x.s.Sq + 1) : x.s.Sk;
             }
         }
-        const int lim0 = p.causal ? min(x.s.Sk, x.r0 / p.group + x.s.Sk - x.s.Sq + 1) : x.s.Sk;  // the least
+        const int lim0 = p.causal ? min(x.s.Sk, p.by_group.quotient(x.r0) + x.s.Sk - x.s.Sq + 1) : x.s.Sk;  // the least
 
         for (int g = x.g0; g < x.g1; ++g) {
             const uint32_t at0 = static_cast<uint32_t>(g) * C::GR + w * C::TS;
@@ -1015,7 +1040,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
             }
         const bool whole = x.first && x.last;
         const size_t piece = (2 * static_cast<size_t>(blockIdx.x) + (x.first ? 1 : 0)) * C::ROWS;
-        const int h0 = (x.u % p.pool.Hkv) * p.group;
+        const int h0 = p.by_hkv.remainder(x.u) * p.group;
         float* buf = reinterpret_cast<float*>(smem + C::OFF_RED);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1052,7 +1077,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                         if (z.y != 0.0f) sum += z.y * ex2_sfu(z.x - top);  // a NaN stays one
                     }
                     if (whole) {
-                        const int tok = r / p.group, h = h0 + r - tok * p.group;
+                        const int tok = p.by_group.quotient(r), h = h0 + r - tok * p.group;
                         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) acc[i] *= inv;
@@ -1074,7 +1099,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         if (!whole && x.first && threadIdx.x == 0) {
             // the pieces that follow are in the ranges up to the one that holds the unit's end
             const long long end = start.hi + x.left;
-            const long long last = (end * gridDim.x + start.total - 1) / start.total - 1;
+            const long long last = divide(end * gridDim.x + start.total - 1, start.total) - 1;
             p.rec[blockIdx.x] = PagedRecord{x.b, x.u, static_cast<int>(last), 0};
         }
     }
@@ -1143,12 +1168,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q0 = p.cu_q[rec.b];
     const int Sq = max(0, min(p.cu_q[rec.b + 1] - q0, p.max_q));
-    const int r0 = (rec.u / p.pool.Hkv) * ROWS, rows = min(ROWS, Sq * p.group - r0);
-    const int h0 = (rec.u % p.pool.Hkv) * p.group;
+    const int r0 = p.by_hkv.quotient(rec.u) * ROWS, rows = min(ROWS, Sq * p.group - r0);
+    const int h0 = p.by_hkv.remainder(rec.u) * p.group;
     float acc[D / 32], m, l;
     const bool few = gridDim.y == 1 && rec.last - static_cast<int>(blockIdx.x) < kJoinFew;
     for (int row = few ? w : blockIdx.y; row < rows; row += few ? kJoinWarps : gridDim.y) {
-        const int tok = (r0 + row) / p.group, h = h0 + r0 + row - tok * p.group;
+        const int tok = p.by_group.quotient(r0 + row), h = h0 + r0 + row - tok * p.group;
         uint16_t* const dst = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(q0 + tok) * p.Hq + h) * D;
         float* const lse = p.lse + static_cast<size_t>(h) * p.total_q + q0 + tok;
         if (few) {
