@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                     }
                 }
             } else {
-#pragma unroll
+#pragma unroll 1
                 for (int k4 = 0; k4 < D / 32; k4 += (D % 128 == 0 ? 4 : 2)) {
                     constexpr int KG = D % 128 == 0 ? 4 : 2;  // groups per load of pairs
                     uint32_t pr[MB][2][KG];
