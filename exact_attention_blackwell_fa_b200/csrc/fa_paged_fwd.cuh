@@ -170,9 +170,9 @@ constexpr int kPagedCtas = 2;
 
 template <int D, bool INT4, int NT>
 struct PagedCfg {
-    static constexpr int TS = INT4 ? 32 : 16;      // tokens of a warp's step
+    static constexpr int TS = INT4 && D < 384 ? 32 : 16;  // tokens of a warp's step
     static constexpr int MB = TS / 16;
-    static constexpr int W = D == 128 && NT == 1 ? 6 : 4;  // warps
+    static constexpr int W = INT4 && D >= 384 ? 8 : D == 128 && NT == 1 ? 6 : 4;  // warps
     static constexpr int ROWS = 8 * NT;
     static constexpr int GR = W * TS;              // tokens of a granule
     static constexpr int RB = INT4 ? D / 2 : 2 * D;  // bytes of a row (codes)
