@@ -371,13 +371,13 @@ def _check_cache(k_cache, v_cache, dtype, block_table, device):
     """Validates a pair of pools and their block table; returns (num_pages, Hkv,
     page_size, d, fmt, B, max_pages).  Pools are [num_pages, Hkv, page_size, d] in the
     call's dtype, or uint8 [num_pages, Hkv, page_size, 5 d / 8]."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+    for t in (k_cache, v_cache):
         if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
-            raise ValueError(f"fa: {name} must be a contiguous tensor on {device}")
+            raise ValueError(f"fa: k_cache and v_cache must be contiguous tensors on {device}")
     shape, kind = k_cache.shape, k_cache.dtype
-    if kind != v_cache.dtype or (kind != dtype and kind != torch.uint8):
+    if v_cache.dtype != kind or (kind != dtype and kind != torch.uint8):
         raise ValueError(f"fa: the pools have dtypes {kind} and {v_cache.dtype}, expected {dtype} or uint8")
-    if len(shape) != 4 or shape != v_cache.shape:
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("fa: k_cache and v_cache must be [num_pages, Hkv, page_size, d] (4-bit: 5 d / 8 bytes)")
     num_pages, Hkv, page_size, width = shape
     fmt = FA_KV_16
@@ -385,10 +385,10 @@ def _check_cache(k_cache, v_cache, dtype, block_table, device):
         if width % 5:
             raise ValueError(f"fa: a 4-bit pool has 5 d / 8 bytes per token, got {width}")
         width, fmt = width * 8 // 5, FA_KV_INT4
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("fa: block_table must be a [B, max_pages] tensor")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.dtype != torch.int32 or \
+            block_table.device != device or not block_table.is_contiguous():
+        raise ValueError(f"fa: block_table must be a contiguous int32 [B, max_pages] tensor on {device}")
     B, max_pages = block_table.shape
-    _check_index(block_table, "block_table", (B, max_pages), device)
     return num_pages, Hkv, page_size, width, fmt, B, max_pages
 
 
@@ -441,7 +441,7 @@ def fa_kv_append(q, k, v, k_cache, v_cache, cu_seqlens, seqlens_k, block_table, 
         _same_device(k, inv_freq=inv_freq)
     with _on(device, stream):
         if q is not None and q_out is None:
-            q_out = q.new_empty((total, Hq, d))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         code = _lib.load().fa_kv_append(
             q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
             q_out.data_ptr() if q is not None else None, k_cache.data_ptr(), v_cache.data_ptr(),
