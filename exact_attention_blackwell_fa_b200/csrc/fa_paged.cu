@@ -132,11 +132,11 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     int grid = C::CTAS * sm_count;
     // Few short sequences: a unit stays whole, and nothing is left to join.  Up to about
     // 160 KB of keys and values one CTA takes no longer than the pieces and their join (one
-    // sequence, 8 KV heads, d = 128: 64 / 256 / 384 / 512 tokens 6.2 / 8.6 / 9.7 / 11.4 us
-    // whole, 7.2 / 9.2 / 9.1 / 9.2 us in pieces), and a launch less is 2 us of host time.
-    // 4-bit rows take longer to expand than to read: one or two granules (d = 128, 256
-    // tokens: 9.2 us against 10.2; d = 512: 19.6 against 18.2, 128 tokens 14.7 against 16.2)
-    const bool whole = units <= grid && (INT4 ? granules <= (D <= 256 ? 2 : 1) : keys * 4 * D <= 160 * 1024);
+    // sequence, 8 KV heads, d = 128: 64 / 256 / 384 / 512 tokens 5.9 / 8.1 / 9.2 / 11.2 us
+    // whole, 6.9 / 8.9 / 8.9 / 8.9 us in pieces), and a launch less is 2 us of host time.
+    // 4-bit rows take longer to expand than to read: two granules (d = 128, 256 tokens: 8.8
+    // us against 9.9; d = 512, 256 tokens: 17.0 against 17.7)
+    const bool whole = units <= grid && (INT4 ? granules <= 2 : keys * 4 * D <= 160 * 1024);
     fa::PagedFwdParams a = p;
     a.coarse = whole ? static_cast<int>(granules) : 1;
     if (whole) a.rec = nullptr;
@@ -151,8 +151,8 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     // a block per cut unit; where pieces per unit are many, or blocks few, a block per row
-    // of it (b = 1, 1000 tokens, 8 KV heads: 10.4 us against 12.2 in all; 64 sequences up to
-    // 8192 tokens, 4 KV heads: 94.3 us with a block per row, 91.2 with one)
+    // of it (one sequence of 1000 tokens, 8 KV heads: 9.3 us in all against 13.3; 64
+    // sequences up to 8192 tokens, 4 KV heads: 94.7 us with a block per row, 93.9 with one)
     cfg.gridDim = dim3(grid, units * 8 < grid || grid * C::ROWS <= 1024 ? C::ROWS : 1);
     cfg.blockDim = dim3(fa::kJoinWarps * 32);
     cfg.stream = s;

@@ -106,6 +106,11 @@ __device__ __forceinline__ void find_sequences(const int* cu, int B, int t0, int
 // integer product drops whole turns), whatever the position; the error is inv_freq's
 // rounding to 2^-53 relative, times the position.
 //
+// Measured: 12,313 tokens, 32/8 heads of 128, 16-bit pages: 52 us, 5.9 TB/s; 15,530
+// tokens, 32/4 heads, 4-bit pages: 75 us, bound by issue (keys are turned and coded in 64
+// bits); 32 tokens: 3.4 us, the latency of three loads in turn.  Four tokens per block
+// beat two (54 against 58 us) and eight (56).
+//
 // A row is cut into items of two 16-byte vectors that hold both members of their pairs
 // (half-split pairs: vectors i and i + rot / 16; interleaved or not rotated: two
 // neighbours), so that a thread can overwrite what it read (q_out = q).

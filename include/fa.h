@@ -199,8 +199,9 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
  *
  * A token whose block table entry is not a page of the pool, or whose position is not
  * in the table (negative, or max_pages * page_size and up), is not written by
- * fa_kv_append, reads as zeros in fa_kv_gather and is left out of fa_fwd_paged; nothing
- * outside the pool is touched, and the device status becomes FA_ERR_BAD_PAGE.
+ * fa_kv_append (its query is turned all the same), reads as zeros in fa_kv_gather and is
+ * left out of fa_fwd_paged; nothing outside the pool is touched, and the device status
+ * becomes FA_ERR_BAD_PAGE.
  */
 typedef enum { FA_KV_16 = 0, FA_KV_INT4 = 1 } fa_kv_format;
 
