@@ -355,7 +355,10 @@ def _on(device, stream=None):
     that stream still uses it."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+                torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"fa: the stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
     return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 

@@ -673,6 +673,10 @@ def test_explicit_streams_and_two_calls_at_once():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     ref = torch.cat([c.rows(c.k, b, n) for b, n in enumerate(lens)])
     assert torch.equal(k.double(), ref)
+    for s in (0, torch.cuda.default_stream()):
+        o, lse = fa.fa_fwd_paged(qs[0], c.k, c.v, cu, sk, c.table, 1, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0][0]) and torch.equal(lse, want[0][1])
     x = randn(2, 2, d, seed=5)
     fa.fa_kv_append(None, x, x, c.k, c.v, cu, sk, c.table, stream=streams[1])
     torch.cuda.synchronize()
