@@ -1,0 +1,73 @@
+"""Paged KV cache at the edges of the types' ranges: small softmax weights, infinities among
+the values, 4-bit groups and queries of the largest magnitudes; each against its definition
+in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from test_paged import (BF16, FP16, NAN, Cache, attend, check_paged, cu_of, fa_mod, half, held, i32, quantise, randn,
+                        status_ok, turn)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("d,Hq,Hkv,lens", [(128, 8, 2, [3000, 60]), (256, 4, 1, [1500]), (512, 2, 2, [700, 33])])
+def test_small_weights_beside_dominating_keys(d, Hq, Hkv, lens, dt, int4):
+    """Every 16th key dominates and its value is 0: the output is what the others, 12 to 20
+    nats below, weigh."""
+    fa, n = fa_mod(), sum(lens)
+    g = torch.Generator().manual_seed(d)
+    for gap in (12.0, 15.0, 17.0, 20.0):
+        c = Cache(lens, Hkv, d, 32, int4, dt)
+        k, v = torch.zeros(n, Hkv, d), 20000.0 + 500.0 * torch.randn(n, Hkv, d, generator=g)
+        k[..., 0] = (0.3 * torch.randn(n, Hkv, generator=g) - gap) / 4
+        k[5::16] = 0.0
+        v[5::16] = 0.0
+        fa.fa_kv_append(None, k.to(dt).cuda(), v.to(dt).cuda(), c.k, c.v, cu_of(lens), i32(lens), c.table)
+        rows = [(c.rows(c.k, b, m), c.rows(c.v, b, m)) for b, m in enumerate(lens)]
+        q = torch.zeros(len(lens), Hq, d, dtype=dt, device="cuda")
+        q[..., 0] = 4.0
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu_of([1] * len(lens)), i32(lens), c.table, 1, scale=1.0)
+        status_ok(fa)
+        for b, m in enumerate(lens):
+            ro, rl, mass = attend(q[b: b + 1].double(), *rows[b], False, 1.0)
+            # scores: one product each, summed with zeros (4 bits: scale * code and zero, each
+            # rounded, and their sum) and scaled, four roundings of 2^-24 of at most 21 * log2 e;
+            # exponentials, row sum and division 2^-21
+            err = 4 * 2.0 ** -24 * 31 + 2.0 ** -21
+            # a weight is held in two terms of the type: bf16 to 2^-16 of itself; fp16 to 2^-20
+            # of itself or half its least step, 2^-25, where the largest weight is at least 2^14
+            held_to = 2.0 ** -16 if dt == BF16 else 2.0 ** -20
+            floor = 0.0 if dt == BF16 else m * 2.0 ** -39 * rows[b][1].abs().max()
+            bound = half(dt) * 1.01 * ro.abs() + (err + held_to + (half(dt) * 1.01 if int4 else 0)) * mass + floor + 2.0 ** -25
+            e = (o[b: b + 1].double() - ro).abs()
+            assert bool((e <= bound).all()), (gap, b, (e / ro.abs()).max().item(), (bound / ro.abs()).max().item())
+            assert ((lse[:, b: b + 1].double() - rl).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("up", [2.0 ** 8, 2.0 ** 9, 2.0 ** 10, 2.0 ** 11, 2.0 ** 13])
+def test_fp16_scores_further_apart_than_the_reference(up, int4):
+    """Scores of 2^16 to 2^30, where 32 bits step by more than what lies between the reference
+    and the greatest score: weights stay inside fp16, and the greatest score's value comes out."""
+    fa, d, n, dt = fa_mod(), 128, 600, FP16
+    c = Cache([n], 2, d, 32, int4, dt)
+    k, v = randn(n, 2, d, seed=1, dt=dt) * up, randn(n, 2, d, seed=2, dt=dt)
+    fa.fa_kv_append(None, k, v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+    rows = c.rows(c.k, 0, n), c.rows(c.v, 0, n)
+    q = randn(1, 16, d, seed=3, dt=dt) * up
+    o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 1]), i32([n]), c.table, 1, scale=1.0)
+    status_ok(fa)
+    x = torch.einsum("hd,jhd->hj", q[0].double(), rows[0].repeat_interleave(8, 1))
+    size = torch.einsum("hd,jhd->hj", q[0].double().abs(), rows[0].abs().repeat_interleave(8, 1)).amax(-1)
+    best, order = x.sort(-1, descending=True)
+    off = size * d * 2.0 ** -23                          # of a score: d products summed in fp32
+    assert o.isfinite().all() and ((lse[:, 0].double() - best[:, 0]).abs() <= off + 2.0 ** -21 * best[:, 0].abs() + 1).all()
+    alone = best[:, 0] - best[:, 1] > 2 * off + 40       # the others weigh nothing
+    assert alone.any()
+    for h in alone.nonzero()[:, 0].tolist():
+        want = rows[1][order[h, 0], h // 8]
+        assert ((o[0, h].double() - want).abs() <= 2.02 * half(dt) * want.abs() + 2.0 ** -24).all()
