@@ -48,6 +48,7 @@
 // instructions per 32 tokens of keys and values, where streaming alone takes 57 us.
 #pragma once
 
+#include <cfloat>
 #include <utility>
 
 #include "fa_paged.cuh"
@@ -697,6 +698,104 @@ __device__ __forceinline__ void paged_product_by_token(const uint8_t* vs, int ba
 }
 
 // ---------------------------------------------------------------------------------
+// What an output is that did not come out finite.  An infinity among the values times a
+// weight in two terms is a NaN where the second is 0 or negative, or where the weight is
+// too small for 32 bits; by the definition (a finite score's weight is above 0) it stays
+// that infinity.  So the answer depends on no weight: +infinity, -infinity, or a NaN where
+// the row sees one or both signs.  Looking at the values of every tile would cost each
+// step; this looks at a row's again after the range, only where an output calls for it.
+// Out of line and after the loop, where its registers are free, it costs calls without
+// infinities 0 to 1 % (d = 512: 2 %); within the loop it cost 1 to 10 %.
+// ---------------------------------------------------------------------------------
+struct PagedValues {
+    const uint8_t* pool;  // of the KV head, at page 0
+    const int* table;     // of the sequence
+    size_t page_bytes;    // from one page to the next
+    int shift, num_pages;
+};
+// For dims 8 v .. 8 v + 7 of the tokens from .. to - 1 (from: a multiple of 16) two bits
+// each: 1 if one of them is +infinity, 2 if one is -infinity, 3 for both or a NaN.
+template <int D, bool BF16, bool INT4>
+__device__ uint32_t paged_not_finite(const PagedValues& at, int from, int to, int v)
+{
+    constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u;
+    constexpr int RB = INT4 ? D / 2 : 2 * D;
+    uint32_t found = 0;
+    for (long long j = from; j < to && found != 0xffffu; j += 16) {
+        const int page = at.table[j >> at.shift];
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(at.num_pages)) continue;
+        const int slot = static_cast<int>(j) & ((1 << at.shift) - 1), n = static_cast<int>(min(16ll, to - j));
+        const uint8_t* const block = at.pool + page * at.page_bytes;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const uint8_t* const row = block + static_cast<size_t>(slot + i) * RB;
+            const uint4 x = read_vector<D, BF16, INT4>(row, block + (static_cast<size_t>(RB) << at.shift) + (slot + i) * (D / 8), v);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t y = k & 1 ? u[k / 2] >> 16 : u[k / 2] & 0xffffu;
+                if ((y & EXP) == EXP) found |= ((y & 0x7fffu) != EXP ? 3u : y & 0x8000u ? 2u : 1u) << (2 * k);
+            }
+        }
+    }
+    return found;
+}
+
+// A range's outputs (or pieces of them) as the join of the warps has written them: the
+// same thread looks at what it wrote.
+template <int D, bool BF16, bool INT4, int NT>
+__device__ __noinline__ void paged_settle(const PagedFwdParams& p, const PagedStart& start)
+{
+    using C = PagedCfg<D, INT4, NT>;
+    PagedWalk<C> walk;
+    PagedSegment x;
+    walk.init(p, start);
+    while (walk.next(p, x)) {
+        const bool whole = x.first && x.last;
+        const size_t piece = (2 * static_cast<size_t>(blockIdx.x) + (x.first ? 1 : 0)) * C::ROWS;
+        const int hkv = p.by_hkv.remainder(x.u);
+        const PagedValues at{static_cast<const uint8_t*>(p.v_cache) + static_cast<size_t>(hkv) * p.block_bytes,
+                             p.pool.table + static_cast<size_t>(x.b) * p.pool.max_pages,
+                             static_cast<size_t>(p.block_bytes) * p.pool.Hkv, p.pool.page_shift, p.pool.num_pages};
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll 1
+            for (int part = 0; part < D / C::DP; ++part) {
+#pragma unroll 1
+                for (int y = threadIdx.x; y < C::DP; y += C::THREADS) {
+                    const int rr = y / (C::DP / 8), v = part * (C::DP / 8) + y - rr * (C::DP / 8), r = x.r0 + nt * 8 + rr;
+                    if (r >= x.R) continue;
+                    const int tok = p.by_group.quotient(r), h = hkv * p.group + r - tok * p.group;
+                    uint16_t* const o = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(x.s.q0 + tok) * p.Hq + h) * D + v * 8;
+                    float* const partial = p.opart + (piece + nt * 8 + rr) * D + v * 8;
+                    const float sum = whole ? p.lse[static_cast<size_t>(h) * p.total_q + x.s.q0 + tok] : p.mlpart[piece + nt * 8 + rr].y;
+                    float acc[8], odd = 0.0f;
+                    if (whole) pg_unpack8<BF16>(*reinterpret_cast<const uint4*>(o), acc);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!whole) acc[i] = partial[i];
+                        odd = fmaf(acc[i], 0.0f, odd);
+                    }
+                    if (!(odd != 0.0f) || !isfinite(sum)) continue;
+                    // the row's tokens among the segment's
+                    const long long seen = p.causal ? min(x.s.Sk, tok + x.s.Sk - x.s.Sq + 1) : x.s.Sk;
+                    const long long end = min(static_cast<long long>(x.g1) * C::GR, seen);
+                    const uint32_t found = paged_not_finite<D, BF16, INT4>(
+                        at, static_cast<int>(min(static_cast<long long>(x.g0) * C::GR, end)), static_cast<int>(end), v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t is = found >> (2 * i) & 3u;
+                        if (is) acc[i] = is == 3u ? NAN : is == 1u ? INFINITY : -INFINITY;
+                        if (!whole) partial[i] = acc[i];
+                    }
+                    if (whole) *reinterpret_cast<uint4*>(o) = pg_pack8<BF16>(acc);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------
 template <int D, bool BF16, bool INT4, int NT>
@@ -710,8 +809,10 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PagedStart start;
     __shared__ long long red[33];
+    __shared__ int unsettled;  // whether an output of the range is not finite though its weights are
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gg = lane >> 2, t = lane & 3;
     const uint32_t sbase = smem_u32(smem);
+    if (threadIdx.x == 0) unsettled = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     paged_start<C>(p, &start, red);
@@ -1098,6 +1199,9 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
                         const float2 z = ml[ww * C::ROWS + nt * 8 + rr];
                         if (z.y != 0.0f) sum += z.y * ex2_sfu(z.x - top);  // a NaN stays one
                     }
+                    // not finite if one of them is not
+                    const float odd = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+                    if (!isfinite(odd) && isfinite(sum)) unsettled = 1;
                     if (whole) {
                         const int tok = p.by_group.quotient(r), h = h0 + r - tok * p.group;
                         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -1126,6 +1230,8 @@ __global__ void __launch_bounds__(PagedCfg<D, INT4, NT>::THREADS, PagedCfg<D, IN
         }
     }
     copy_wait<0>();
+    __syncthreads();
+    if (unsettled) paged_settle<D, BF16, INT4, NT>(p, start);
 }
 
 // ---------------------------------------------------------------------------------
@@ -1157,8 +1263,9 @@ __device__ __forceinline__ void join_pieces(const PagedFwdParams& p, int last, i
 #pragma unroll
         for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         mn = fmaxf(mn, m);
-        const float a = l == 0.0f ? 0.0f : ex2_sfu(m - mn);
-        const float b = z.y == 0.0f ? 0.0f : ex2_sfu(z.x - mn);
+        // at least the least number, so that an infinity among the pieces stays one
+        const float a = l == 0.0f ? 0.0f : fmaxf(ex2_sfu(m - mn), FLT_MIN);
+        const float b = z.y == 0.0f ? 0.0f : fmaxf(ex2_sfu(z.x - mn), FLT_MIN);
         float sum = z.y * b;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -1217,7 +1324,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa_fwd_paged_join_kernel(cons
         for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, ml[i].x);
 #pragma unroll
         for (int i = 0; i < kJoinWarps; ++i) {
-            f[i] = ml[i].y == 0.0f ? 0.0f : ex2_sfu(ml[i].x - top);
+            f[i] = ml[i].y == 0.0f ? 0.0f : fmaxf(ex2_sfu(ml[i].x - top), FLT_MIN);
             sum += ml[i].y * f[i];
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

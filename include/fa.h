@@ -249,7 +249,9 @@ fa_status fa_kv_gather(const void* k_cache, const void* v_cache, void* k, void* 
  * table as max_pages * page_size (with the device status set).  max_seqlen_q bounds the
  * queries per sequence (longer ones are cut to it).  A row that sees no key gets O = 0
  * and LSE = -inf.  What the pools hold past a sequence's end is not used,
- * and an infinity or a NaN in a token reaches only the queries that see it.  `workspace` is
+ * and an infinity or a NaN in a token reaches only the queries that see it: among the
+ * values, an infinity makes their outputs that infinity, however small its weight, and
+ * infinities of both signs, or a NaN, make them NaN.  `workspace` is
  * caller-owned device memory of at least fa_fwd_paged_workspace_size(...) bytes, 256-byte
  * aligned; its contents on entry do not matter, and calls that overlap on the GPU need
  * one each.  Repeated calls give the same bits.  The pages are read once for 8 to 32

@@ -71,3 +71,81 @@ def test_fp16_scores_further_apart_than_the_reference(up, int4):
     for h in alone.nonzero()[:, 0].tolist():
         want = rows[1][order[h, 0], h // 8]
         assert ((o[0, h].double() - want).abs() <= 2.02 * half(dt) * want.abs() + 2.0 ** -24).all()
+
+
+def check_infinite(dims, o, lse, c, rows, q, news, lens, causal, scale):
+    """dims: {dim: what every output holds there}; the other dims and the LSE are the definition's."""
+    o, rows = o.clone(), [(k, v.clone()) for k, v in rows]
+    for dim, want in dims.items():
+        got = o[..., dim].float()
+        assert got.isnan().all() if math.isnan(want) else (got == want).all(), (dim, want, got)
+        o[..., dim] = 0
+        for _, v in rows:
+            v[..., dim] = 0
+    check_paged(c, rows, q, news, lens, causal, scale, o, lse)
+
+
+@pytest.mark.parametrize("d,group,dt", [(128, 4, BF16), (128, 8, FP16), (128, 1, BF16), (192, 2, FP16), (256, 8, BF16),
+                                        (384, 3, FP16), (512, 1, BF16)])
+@pytest.mark.parametrize("n,m", [(1, 1), (2, 1), (70, 1), (70, 6), (3000, 1), (2000, 11)])
+def test_infinite_values_stay_infinities(n, m, d, group, dt):
+    """An infinity among the values that a row sees gives that infinity, in whichever token
+    and whatever its weight; two of both signs give NaN, and a NaN itself."""
+    fa = fa_mod()
+    scale = d ** -0.5
+    for at in sorted({0, 1 % n, n // 2, n - m}):
+        c = Cache([n], 2, d, 16, False, dt)
+        k, v = randn(n, 2, d, seed=1, dt=dt), randn(n, 2, d, seed=2, dt=dt)
+        q = randn(m, 2 * group, d, seed=3, dt=dt)
+        v[at, :, 5], v[at, :, d - 1] = math.inf, -math.inf
+        v[at, :, 40] = math.inf
+        v[(at + 1) % n, :, 40] = -math.inf if n > 1 and at + 1 <= n - m else math.inf
+        v[at, :, 70] = NAN
+        fa.fa_kv_append(None, k, v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+        rows = [(c.rows(c.k, 0, n), c.rows(c.v, 0, n))]
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, m]), i32([n]), c.table, m, causal=True, scale=scale)
+        status_ok(fa)
+        dims = {5: math.inf, d - 1: -math.inf, 40: NAN if n > 1 and at + 1 <= n - m else math.inf, 70: NAN}
+        check_infinite(dims, o, lse, c, rows, q, [m], [n], True, scale)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("gap", [10.0, 25.0, 80.0, 200.0])
+@pytest.mark.parametrize("n,at", [(200, 150), (200, 3), (5000, 20), (5000, 4000)])
+def test_infinite_values_of_small_weight(n, at, gap, dt):
+    """The token that holds the infinity lies far below the others' scores, before or after
+    them, also where its weight is none in 32 bits."""
+    fa, d = fa_mod(), 128
+    c = Cache([n], 1, d, 64, False, dt)
+    k, v = torch.zeros(n, 1, d), randn(n, 1, d, seed=2, dt=dt)
+    k[at, 0, 0] = -gap / 4
+    v[at, 0, 9] = -math.inf
+    fa.fa_kv_append(None, k.to(dt).cuda(), v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+    rows = [(c.rows(c.k, 0, n), c.rows(c.v, 0, n))]
+    q = torch.zeros(1, 4, d, dtype=dt, device="cuda")
+    q[..., 0] = 4.0
+    o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 1]), i32([n]), c.table, 1, scale=1.0)
+    status_ok(fa)
+    check_infinite({9: -math.inf}, o, lse, c, rows, q, [1], [n], False, 1.0)
+
+
+def test_infinite_values_in_some_sequences_of_a_batch():
+    """Sequences with an infinity beside others, several per CTA and cut over several CTAs:
+    the others come out as without them."""
+    fa, d, Hq, Hkv = fa_mod(), 128, 8, 2
+    lens = [(53 * b) % 300 + 1 for b in range(150)] + [4000, 2500, 4000]
+    c = Cache(lens, Hkv, d, 16, False, BF16)
+    k, v = randn(sum(lens), Hkv, d, seed=1), randn(sum(lens), Hkv, d, seed=2)
+    cu, one, sk = cu_of(lens), cu_of([1] * len(lens)), i32(lens)
+    q = randn(len(lens), Hq, d, seed=3)
+    fa.fa_kv_append(None, k, v, c.k, c.v, cu, sk, c.table)
+    clean = [t.clone() for t in fa.fa_fwd_paged(q, c.k, c.v, one, sk, c.table, 1)]
+    hit = list(range(0, 150, 7)) + [151]
+    at = torch.tensor([cu[b].item() + lens[b] // 3 for b in hit], device="cuda")
+    v[at, 1, 17] = math.inf
+    fa.fa_kv_append(None, k, v, c.k, c.v, cu, sk, c.table)
+    o, lse = fa.fa_fwd_paged(q, c.k, c.v, one, sk, c.table, 1)
+    status_ok(fa)
+    want = clean[0].clone()
+    want[torch.tensor(hit, device="cuda"), 4:, 17] = math.inf
+    assert torch.equal(o, want) and torch.equal(lse, clean[1])
