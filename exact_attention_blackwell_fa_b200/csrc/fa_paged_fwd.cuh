@@ -617,7 +617,9 @@ __device__ __forceinline__ int token_of_slot(int slot)
     return C::RBS == 64 && INT4 ? (slot & ~3) | ((slot & 1) << 1) | ((slot >> 1) & 1) : slot;
 }
 
-// Whether a slot's values (4-bit: scales and zeros) hold an infinity or a NaN.
+// Whether a slot's values hold an infinity or a NaN.  4 bits: whether a pair makes the
+// lowest or the highest code one (finite fp16 pairs can: 8736 * 15 - 65504 = 65536); the
+// other codes lie between.
 template <int D, bool BF16, bool INT4, class C>
 __device__ __forceinline__ bool paged_slot_bad(const uint8_t* vs)
 {
@@ -627,7 +629,11 @@ __device__ __forceinline__ bool paged_slot_bad(const uint8_t* vs)
     bool bad = false;
 #pragma unroll 1
     for (int i = (threadIdx.x & 31) * 4; i < BYTES; i += 128) {
-        const uint32_t w = lds<uint32_t>(from + i);
+        uint32_t w = lds<uint32_t>(from + i);
+        if constexpr (INT4) {
+            const float2 sz = pg_unpack2<BF16>(w);
+            w = pg_pack2<BF16>(sz.y, fmaf(15.0f, sz.x, sz.y));
+        }
         bad |= (w & EXP) == EXP || (w >> 16 & EXP) == EXP;
     }
     return __any_sync(0xffffffffu, bad);

@@ -187,7 +187,8 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
  *     On writing, zero is the group's least value and scale a fifteenth of what the
  *     greatest lies above that zero, each rounded to the dtype, and c the nearest whole
  *     number (ties to even, 0 to 15) of scales above the zero.  A group that holds an
- *     infinity or a NaN, or whose scale or zero rounds to one, reads back as NaN.
+ *     infinity or a NaN, or whose scale or zero rounds to one, reads back as NaN; a code
+ *     that stands for more than the dtype holds reads back as an infinity.
  * Pools are addressed with 64-bit offsets.  block_table, seqlens_k and the cu_seqlens
  * arrays are device int32 arrays that the host does not read, so a captured graph can
  * be replayed with new lengths and pages (max_seqlen_q and the row totals of a call

@@ -149,3 +149,31 @@ def test_infinite_values_in_some_sequences_of_a_batch():
     want = clean[0].clone()
     want[torch.tensor(hit, device="cuda"), 4:, 17] = math.inf
     assert torch.equal(o, want) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("d,group", [(128, 4), (192, 1), (256, 3), (512, 2)])
+def test_int4_values_that_round_to_an_infinity(d, group):
+    """fp16 groups whose scale and zero are finite and whose highest code stands for more
+    than the type holds: infinite as the read-back has it, for the rows that see the token."""
+    fa, n, m, dt = fa_mod(), 70, 4, FP16
+    for at in (69, 67, 10):
+        c = Cache([n], 1, d, 16, True, dt)
+        k, v = randn(n, 1, d, seed=1, dt=dt), randn(n, 1, d, seed=2, dt=dt)
+        v[at, 0, :32] = torch.linspace(-1, 1, 32, device="cuda") * torch.finfo(dt).max
+        q = randn(m, group, d, seed=3, dt=dt)
+        fa.fa_kv_append(None, k, v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+        rows = [(c.rows(c.k, 0, n), c.rows(c.v, 0, n))]
+        assert rows[0][1].abs().max() == 65536                  # 8736 * 15 - 65504
+        _, back = fa.fa_kv_gather(c.k, c.v, i32([0, n]), c.table, n, dt)
+        dims = back[at, 0].isinf().nonzero()[:, 0].tolist()
+        assert dims and max(dims) == 31
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, m]), i32([n]), c.table, m, causal=True)
+        status_ok(fa)
+        first = max(0, at - (n - m))
+        if first:
+            clean = [(rows[0][0][: n - m + first], rows[0][1][: n - m + first])]
+            check_paged(c, clean, q[:first], [first], [n - m + first], True, d ** -0.5, o[:first], lse[:, :first])
+        seen = o[first:].float()
+        assert (seen[..., dims] == math.inf).all() and lse.isfinite().all()
+        other = [i for i in range(d) if i not in dims]
+        assert seen[..., other].isfinite().all()
