@@ -205,13 +205,16 @@ __device__ __forceinline__ uint32_t quantise8(const T (&x)[8], uint32_t& pair)
         return 0u;
     }
     if (!(scale > 0.0f)) return 0u;
-    // a power of two keeps the quotient's terms inside the 32-bit range for any scale
-    const float up = scale < 1.0f ? 0x1p100f : 0x1p-100f;
-    const float inv = 1.0f / (scale * up);
+    // Powers of two keep the quotient's terms inside the 32-bit range for any scale.  Where
+    // scales are large so may the values be, and a difference of two reaches twice the range
+    // (turned keys: 2.5 times): a sixteenth of it is formed, by one multiply-add
+    const T part = scale < 1.0f ? T(1) : T(0.0625), low = static_cast<T>(zero) * part;
+    const float up = scale < 1.0f ? 0x1p100f : 0x1p-96f;
+    const float inv = 1.0f / (scale * (scale < 1.0f ? 0x1p100f : 0x1p-100f));
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = static_cast<float>(x[i] - static_cast<T>(zero)) * up * inv;
+        const float q = static_cast<float>(fma(x[i], part, -low)) * up * inv;
         const float r = fminf(fmaxf(q, 0.0f), 15.0f);
         const float t = r + 12582912.0f;  // 1.5 * 2^23: rounds to a whole number
         uint32_t c = __float_as_uint(t) & 15u;

@@ -177,3 +177,30 @@ def test_int4_values_that_round_to_an_infinity(d, group):
         assert (seen[..., dims] == math.inf).all() and lse.isfinite().all()
         other = [i for i in range(d) if i not in dims]
         assert seen[..., other].isfinite().all()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_int4_codes_of_the_widest_groups(dt, inter):
+    """Groups whose values lie further apart than the largest number of 32 bits, as values and
+    as turned keys: the codes of the definition."""
+    fa, d, n = fa_mod(), 128, 12
+    big = torch.finfo(dt).max
+    x = torch.zeros(n, 2, d)
+    x[0, 0] = big * torch.linspace(-1, 1, 32).repeat(4)
+    x[0, 1] = big * torch.linspace(1, -1, 32).repeat(4)
+    x[1, 0, :96] = torch.tensor([-0.9, 0.9, 0.3]).repeat(32) * big
+    x[1, 1] = big * torch.cat([torch.linspace(-1, 1, 31), torch.zeros(1)]).repeat(4)
+    x[2] = big * (torch.arange(d) % 2 * 2 - 1)
+    g = torch.Generator().manual_seed(3)
+    x[3:] = big * (2 * torch.rand(n - 3, 2, d, generator=g) - 1)
+    x[9:] *= 0.7                                             # turned pairs stay within the type
+    x = x.to(dt).cuda()
+    assert x.isfinite().all()
+    freq = (3.0 ** (-torch.arange(0, 64, 2).double() / 64)).float().cuda()
+    c = Cache([n], 2, d, 16, True, dt)
+    fa.fa_kv_append(None, x, x, c.k, c.v, i32([0, n]), i32([n]), c.table, inv_freq=freq, interleaved=inter)
+    status_ok(fa)
+    for pool, ref in ((c.v, held(x.double(), dt)), (c.k, held(turn(x, torch.arange(n, device="cuda"), freq, inter), dt))):
+        assert torch.equal(c.rows(pool, 0, n).nan_to_num(nan=1e39), ref.nan_to_num(nan=1e39))
+        assert ref[0].isfinite().all() and ref[9:].isfinite().all()
