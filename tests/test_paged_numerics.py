@@ -204,3 +204,23 @@ def test_int4_codes_of_the_widest_groups(dt, inter):
     for pool, ref in ((c.v, held(x.double(), dt)), (c.k, held(turn(x, torch.arange(n, device="cuda"), freq, inter), dt))):
         assert torch.equal(c.rows(pool, 0, n).nan_to_num(nan=1e39), ref.nan_to_num(nan=1e39))
         assert ref[0].isfinite().all() and ref[9:].isfinite().all()
+
+
+@pytest.mark.parametrize("group", [1, 8, 20])
+@pytest.mark.parametrize("eq,ek,scale", [(118, -114, 0.088), (118, -20, 2.0 ** -103), (100, -105, 2.0), (50, -56, 16.0),
+                                         (0, 0, 0.088)])
+def test_int4_queries_of_large_magnitude(eq, ek, scale, group):
+    """bf16 queries as large as the calls over a 4-bit pool take them, beside rows of ordinary
+    ones."""
+    fa, d, n, dt = fa_mod(), 128, 300, BF16
+    c = Cache([n], 1, d, 32, True, dt)
+    k, v = randn(n, 1, d, seed=1).float() * 2.0 ** ek, randn(n, 1, d, seed=2)
+    fa.fa_kv_append(None, k.to(dt), v, c.k, c.v, i32([0, n]), i32([n]), c.table)
+    rows = [(c.rows(c.k, 0, n), c.rows(c.v, 0, n))]
+    q = randn(1, group, d, seed=3).float().clamp(-1.9, 1.9)
+    q[:, ::2] *= 2.0 ** eq
+    q = q.to(dt)
+    assert q.isfinite().all()
+    o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 1]), i32([n]), c.table, 1, scale=scale)
+    status_ok(fa)
+    check_paged(c, rows, q, [1], [n], False, scale, o, lse)
