@@ -355,7 +355,8 @@ def _on(device, stream=None):
     that stream still uses it."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            handle = _stream_ptr(stream)  # 0 and 1 both name the legacy default stream
+            stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else \
                 torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"fa: the stream is on {stream.device}, the tensors on {device}")

@@ -224,3 +224,30 @@ def test_int4_queries_of_large_magnitude(eq, ek, scale, group):
     o, lse = fa.fa_fwd_paged(q, c.k, c.v, i32([0, 1]), i32([n]), c.table, 1, scale=scale)
     status_ok(fa)
     check_paged(c, rows, q, [1], [n], False, scale, o, lse)
+
+
+def test_stream_arguments():
+    """stream= takes what the library's other calls take: a torch stream, anything with a
+    cuda_stream, a raw handle; 0 and 1 both name the default stream."""
+    fa = fa_mod()
+    c = Cache([500], 2, 128, 16, False, BF16)
+    rows = c.fill([500], seed=1)
+    q, cu, sk = randn(1, 8, 128, seed=2), i32([0, 1]), i32([500])
+    want = fa.fa_fwd_paged(q, c.k, c.v, cu, sk, c.table, 1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    class Holder:
+        cuda_stream = side.cuda_stream
+
+    for s in (side, side.cuda_stream, Holder(), 0, 1, torch.cuda.default_stream()):
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu, sk, c.table, 1, stream=s)
+        k, v = fa.fa_kv_gather(c.k, c.v, i32([0, 500]), c.table, 500, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(k.double(), rows[0][0]) and torch.equal(v.double(), rows[0][1])
+        # what the call allocated belongs to the stream that it ran on
+        on = 0 if s in (0, 1, torch.cuda.default_stream()) else side.cuda_stream
+        with fa._on(c.k.device, s):
+            assert torch.cuda.current_stream().cuda_stream == on
+    status_ok(fa)
