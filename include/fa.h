@@ -248,8 +248,11 @@ fa_status fa_kv_gather(const void* k_cache, const void* v_cache, void* k, void* 
  * [Hq, total_q]) attend over its seqlens_k[b] cached tokens, the causal mask aligned to
  * the bottom right as everywhere.  A negative seqlens_k[b] counts as 0, one beyond the
  * table as max_pages * page_size (with the device status set).  max_seqlen_q bounds the
- * queries per sequence (longer ones are cut to it).  A row that sees no key gets O = 0
- * and LSE = -inf.  What the pools hold past a sequence's end is not used,
+ * queries per sequence; a sequence with more is cut as fa_fwd_varlen cuts it: its first
+ * max_seqlen_q rows are taken as its queries, the mask aligned to the last of these, and
+ * the other rows are not written (give a captured call the most that a replay will have).
+ * A row that sees no key gets O = 0 and LSE = -inf.  What the pools hold past a sequence's
+ * end is not used,
  * and an infinity or a NaN in a token reaches only the queries that see it: among the
  * values, an infinity makes their outputs that infinity, however small its weight, and
  * infinities of both signs, or a NaN, make them NaN.  4-bit values are rounded to the

@@ -251,3 +251,27 @@ def test_stream_arguments():
         with fa._on(c.k.device, s):
             assert torch.cuda.current_stream().cuda_stream == on
     status_ok(fa)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_cut_sequences_are_those_of_the_varlen_forward(int4):
+    """More queries than max_seqlen_q: the first ones are taken as the sequence's queries, the
+    causal mask at their bottom right, as fa_fwd_varlen takes them."""
+    fa, dt = fa_mod(), BF16
+    news, lens, d = [5, 2, 9], [50, 60, 300], 128
+    c = Cache(lens, 2, d, 16, int4, dt)
+    c.fill(lens, seed=1)
+    q = randn(sum(news), 4, d, seed=2, dt=dt)
+    cu, ck = cu_of(news), cu_of(lens)
+    k, v = fa.fa_kv_gather(c.k, c.v, ck, c.table, sum(lens), dt)
+    for most in (2, 4, 9):
+        o, lse = fa.fa_fwd_paged(q, c.k, c.v, cu, i32(lens), c.table, most, causal=True)
+        ro, rl = fa.fa_fwd_varlen(q, k, v, cu, ck, most, max(lens), causal=True)
+        status_ok(fa)
+        at = 0
+        for m in news:
+            r = slice(at, at + min(m, most))
+            # the library's forward bound, on both sides; 4-bit keys are rounded by the read-back
+            assert ((o[r].double() - ro[r].double()).abs() <= 2e-2 + 2 * half(dt) * ro[r].double().abs()).all()
+            assert (lse[:, r] - rl[:, r]).abs().max() <= 2e-3 + (2e-2 if int4 else 0)
+            at += m
