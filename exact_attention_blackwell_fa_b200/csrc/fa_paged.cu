@@ -134,6 +134,9 @@ fa_status launch_paged(const fa::PagedFwdParams& p, int sm_count, cudaStream_t s
     // 160 KB of keys and values one CTA takes no longer than the pieces and their join (one
     // sequence, 8 KV heads, d = 128: 64 / 256 / 384 / 512 tokens 5.9 / 8.1 / 9.2 / 11.2 us
     // whole, 6.9 / 8.9 / 8.9 / 8.9 us in pieces), and a launch less is 2 us of host time.
+    // The host knows the table's width alone, so lengths are taken to be as long as that: a
+    // table of 128 pages of 64 for the same sequence has its units cut (64 / 256 tokens: 8.4 /
+    // 11.0 us against 6.1 / 8.3 with tables of 1 and 4 pages).
     // 4-bit rows take longer to expand than to read: two granules (d = 128, 256 tokens: 8.8
     // us against 9.9; d = 512, 256 tokens: 17.0 against 17.7)
     const bool whole = units <= grid && (INT4 ? granules <= 2 : keys * 4 * D <= 160 * 1024);

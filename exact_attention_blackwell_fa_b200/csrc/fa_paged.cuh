@@ -106,10 +106,11 @@ __device__ __forceinline__ void find_sequences(const int* cu, int B, int t0, int
 // integer product drops whole turns), whatever the position; the error is inv_freq's
 // rounding to 2^-53 relative, times the position.
 //
-// Measured: 12,313 tokens, 32/8 heads of 128, 16-bit pages: 52 us, 5.9 TB/s; 15,530
-// tokens, 32/4 heads, 4-bit pages: 75 us, bound by issue (keys are turned and coded in 64
-// bits); 32 tokens: 3.4 us, the latency of three loads in turn.  Four tokens per block
-// beat two (54 against 58 us) and eight (56).
+// Measured (time on the GPU): 12,313 tokens, 32/8 heads of 128, 16-bit pages: 52 us, 5.9
+// TB/s; 15,530 tokens, 32/4 heads, 4-bit pages: 73 us, 1.6 times its bytes (keys are
+// turned and coded in 64 bits; 60 % of the issue slots and 43 % of the ALU pipe are used);
+// 32 tokens: 4.2 us, the latency of three loads in turn.  Four tokens per block beat two
+// (54 against 58 us) and eight (56).
 //
 // A row is cut into items of two 16-byte vectors that hold both members of their pairs
 // (half-split pairs: vectors i and i + rot / 16; interleaved or not rotated: two
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(256, INT4 ? 6 : 4) fa_kv_gather_kernel(const G
         const uint8_t* const src = static_cast<const uint8_t*>(key ? p.k_cache : p.v_cache) +
                                    static_cast<size_t>(h) * pool_block_bytes<D, INT4>(p.pool);
         uint4* const dst = static_cast<uint4*>(key ? p.k : p.v) + static_cast<size_t>(t0) * row + r;
-        // rows whose loads are in flight together.  4-bit pools: writing is four fifths of the
+        // rows whose loads are in flight together.  4-bit pools: writing is three quarters of the
         // traffic, and one row after the other leaves in order (142 us against 162 with two
         // and 187 with eight, 134,452 tokens of 8 heads of 128); 16-bit: eight (37.5 us
         // against 47 with one, 49,675 tokens of 2 heads of 256)

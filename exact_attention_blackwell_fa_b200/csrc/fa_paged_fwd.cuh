@@ -41,11 +41,14 @@
 // up), and one fused multiply-add gives scale * code + zero with one rounding: the value
 // that the read-back gives.
 //
-// Measured (one B200, copy rate 6548 GB/s): 16-bit, 64 sequences up to 8192 tokens, 32/4
-// heads of 128: 94 us, 5.7 TB/s of keys and values, bound by memory (8 us of it the
-// prologue and the join); 4 x 131,072 tokens, 16/2 heads of 256: 168 us, 6.4 TB/s.  4-bit,
-// 64 sequences, 32/8 heads of 128: 105 us, 2.9 TB/s, bound by issue: about 1000
-// instructions per 32 tokens of keys and values, where streaming alone takes 57 us.
+// Measured (time on the GPU; one B200, copy rate 6548 GB/s): 16-bit, 64 sequences up to
+// 8192 tokens, 32/4 heads of 128: 91 us, 5.9 TB/s of keys and values, bound by memory (8
+// us of it the prologue and the join); 4 x 131,072 tokens, 16/2 heads of 256: 164 us, 6.5
+// TB/s.  4-bit, 64 sequences, 32/8 heads of 128: 103 us, 2.9 TB/s, where streaming alone
+// takes 57 us: about 1000 instructions per 32 tokens of keys and values (22 % of them
+// copies, addresses and page lookups), 58 % of the issue slots and 44 % of the ALU pipe
+// used.  No unit is full: a warp's step is a chain (copy, scores, shuffles, exponentials,
+// values) that 12 warps per SM do not cover.
 #pragma once
 
 #include <cfloat>
@@ -185,7 +188,8 @@ struct PagedCfg {
     // against 98.7 with four and 98.4 with eight; 4-bit 105 us against 120 with five, 127
     // and 123 with seven and eight, which spill).  4-bit rows of 384 and 512 fill the shared
     // memory with few slots: halving the step makes room for twice the warps (d = 512, 32
-    // sequences of 8192 tokens: 82 us against 106)
+    // sequences of 8192 tokens: 82 us against 106).  Two and four tiles take four warps,
+    // whose 255 registers they need; other counts were not measured for them
     static constexpr int TS = INT4 && D < 384 ? 32 : 16;
     static constexpr int MB = TS / 16;
     static constexpr int W = INT4 && D >= 384 ? 8 : D == 128 && NT == 1 ? 6 : 4;
