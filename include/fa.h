@@ -252,15 +252,15 @@ fa_status fa_kv_gather(const void* k_cache, const void* v_cache, void* k, void* 
  * max_seqlen_q rows are taken as its queries, the mask aligned to the last of these, and
  * the other rows are not written (give a captured call the most that a replay will have).
  * A row that sees no key gets O = 0 and LSE = -inf.  What the pools hold past a sequence's
- * end is not used,
- * and an infinity or a NaN in a token reaches only the queries that see it: among the
- * values, an infinity makes their outputs that infinity, however small its weight, and
- * infinities of both signs, or a NaN, make them NaN.  4-bit values are rounded to the
- * dtype before they are weighted, as fa_kv_gather gives them; keys are not.  Over a 4-bit
- * pool a row of bf16 queries must stay below 2^120 in magnitude, and below 2^50 where
- * scale is above 2 (other rows are not touched by one that does not), and a score is off
- * by up to 2^-110 of the keys' magnitude (which tells for queries below 2^-80 only);
- * scales of a pool that the caller fills itself stay below 2^126.  `workspace` is
+ * end is not used, and an infinity or a NaN in a token reaches only the queries that see
+ * it: among the values, an infinity makes their outputs that infinity, however small its
+ * weight, and infinities of both signs, or a NaN, make them NaN.  4-bit values are rounded
+ * to the dtype before they are weighted, as fa_kv_gather gives them; keys are not.  Over a
+ * 4-bit pool a row of bf16 queries must stay below 2^120 in magnitude, and where scale is
+ * above 2 its magnitude times scale below 2^56 (other rows are not touched by one that
+ * does not), and a score is off by up to 2^-110 of the keys' magnitude (which tells for
+ * queries below 2^-80 only); scales of a pool that the caller fills itself stay below
+ * 2^126.  `workspace` is
  * caller-owned device memory of at least fa_fwd_paged_workspace_size(...) bytes, 256-byte
  * aligned; its contents on entry do not matter, and calls that overlap on the GPU need
  * one each.  Repeated calls give the same bits.  The pages are read once for 8 to 32

@@ -208,6 +208,7 @@ def test_int4_codes_of_the_widest_groups(dt, inter):
 
 @pytest.mark.parametrize("group", [1, 8, 20])
 @pytest.mark.parametrize("eq,ek,scale", [(118, -114, 0.088), (118, -20, 2.0 ** -103), (100, -105, 2.0), (50, -56, 16.0),
+                                         (53, -62, 4.0), (44, -60, 1024.0),
                                          (0, 0, 0.088)])
 def test_int4_queries_of_large_magnitude(eq, ek, scale, group):
     """bf16 queries as large as the calls over a 4-bit pool take them, beside rows of ordinary
